@@ -1,6 +1,7 @@
 """Build libswa.so in-tree with nvcc for sm_100a (no JIT cache, no pip install)."""
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -19,6 +20,7 @@ FLAGS = [
     "-cudart", "shared",
     "-Xlinker", "-rpath,/usr/local/cuda/lib64",
 ]
+LINK_FLAGS = FLAGS[-2:]
 
 
 def sources():
@@ -40,12 +42,30 @@ def needs_build() -> bool:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not needs_build():
         return LIB
-    cmd = [NVCC, *FLAGS, *extra, "-I", INCLUDE, "-shared", "-o", LIB + ".tmp", *sources()]
+    # one nvcc per source, side by side; objects newer than their source and every
+    # header are kept
+    objdir = os.path.join(HERE, "_build")
+    os.makedirs(objdir, exist_ok=True)
+    hdr = max(os.path.getmtime(f) for f in headers() + [os.path.abspath(__file__)])
+    flags = [f for f in FLAGS if f not in LINK_FLAGS]
+    jobs, objs = [], []
+    for src in sources():
+        obj = os.path.join(objdir, os.path.basename(src) + ".o")
+        objs.append(obj)
+        if force or extra or not os.path.exists(obj) or os.path.getmtime(obj) <= max(os.path.getmtime(src), hdr):
+            jobs.append(([NVCC, *flags, *extra, "-I", INCLUDE, "-c", "-o", obj + ".tmp", src], obj))
+    with concurrent.futures.ThreadPoolExecutor(max(1, min(len(jobs), os.cpu_count() or 1))) as pool:
+        list(pool.map(lambda j: _run(j[0], j[1], verbose), jobs))
+    _run([NVCC, *FLAGS, "-shared", "-o", LIB + ".tmp", *objs], LIB, verbose)
+    return LIB
+
+
+def _run(cmd, out, verbose):
+    """Run one nvcc command that writes ``out`` + ".tmp", then put the file in place."""
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
-    os.replace(LIB + ".tmp", LIB)
-    return LIB
+    os.replace(out + ".tmp", out)
 
 
 if __name__ == "__main__":
