@@ -339,6 +339,193 @@ swa_status swa_forward_noalloc(const swa_plan_desc* desc, const void* q, const v
                                const int32_t* window, const int32_t* dilation, int causal,
                                const int32_t* valid_len, void* out, float* lse, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions and per-head norms of queries and keys ("SWAN-GPT" §3.3(1):
+ * the sliding-window layers rotate q and k by their positions before the
+ * attention; the fine-tuning recipe §3, hybrid form: only part of the head is
+ * rotated).  For a head row x of D elements at position t:
+ *   u = x / sqrt(mean(x^2) + eps) * weight          (only with norm == 1, else u = x)
+ *   y[a] = A (u[a] cos - u[b] sin),  y[b] = A (u[a] sin + u[b] cos),  angle = t * freq[j]
+ * for every pair j < rotary_dim / 2: (a, b) = (2j, 2j + 1) in the interleaved
+ * layout, (j, j + rotary_dim / 2) in the half layout; elements from rotary_dim on
+ * keep u.  Angles are formed in 64 bits, sums in 32, and y is rounded once.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int rotary_dim;          /* leading elements of the head that rotate: a multiple of 16,
+                              <= head_dim; 0: no rotation */
+  int interleaved;         /* 1: pairs (2j, 2j+1); 0: pairs (j, j + rotary_dim/2) */
+  const double* freq;      /* HOST [rotary_dim / 2] radians per position, finite */
+  float amplitude;         /* A; 0 selects 1 */
+} swa_rotation;
+
+typedef struct {
+  int norm;                /* 1: RMS norm of every q and k head before the rotation; 0: none */
+  float eps;               /* >= 0 */
+  const void* q_weight;    /* device [D], 16-byte aligned, or NULL (all ones) */
+  const void* k_weight;
+  swa_dtype weight_dtype;  /* element type of the weights */
+} swa_head_norm;
+
+/* Strides are in elements, over (batch, head, position); the last axis has stride
+ * 1.  Every pointer is 16-byte aligned and every stride a multiple of 16 bytes, so
+ * a slice of a projection's [B, n, heads, D] output is read as it lies.  Inputs may
+ * have zero strides (broadcast); outputs must not overlap themselves.  An output
+ * may be its own input (same pointer and strides). */
+typedef struct {
+  int batch, seq_len;      /* >= 0; a call without rows launches nothing */
+  int num_q_heads;         /* >= 1 */
+  int num_kv_heads;        /* >= 0; 0: no k */
+  int head_dim;            /* 64 or 128 */
+  swa_dtype dtype;         /* of q, k and the outputs */
+  const void* q;
+  const void* k;
+  int64_t q_stride[3], k_stride[3];
+  const int32_t* positions;   /* device [B, n], or NULL: start, start + 1, ... in every batch */
+  int start;
+  void* q_out;
+  void* k_out;
+  int64_t q_out_stride[3], k_out_stride[3];
+  swa_rotation rotation;
+  swa_head_norm head_norm;
+} swa_rotary_args;
+
+/* One launch on `stream`.  SWA_ERR_INVALID_ARG for a null or misaligned pointer, a
+ * bad size, stride, frequency or eps; SWA_ERR_UNSUPPORTED for head_dim not in
+ * {64, 128} or rotary_dim not a multiple of 16. */
+swa_status swa_rotary_forward(const swa_rotary_args* args, void* stream);
+
+/* Gradients of swa_rotary_forward: dq = d(loss)/dq for dq_out = d(loss)/dq_out (and
+ * k alike).  q and k (the forward's inputs) are read only with norm == 1, and may be
+ * NULL without; then dq_weight / dk_weight [D] fp32 receive the weights' gradients
+ * (NULL: not wanted).  Sums are in fp32 and their order is fixed: the same call gives the
+ * same bits.  The workspace holds the weights' partial sums: at least
+ * swa_rotary_workspace_bytes(args) bytes of device memory, 16-byte aligned, used by
+ * this call only until its kernels have run. */
+typedef struct {
+  int batch, seq_len, num_q_heads, num_kv_heads, head_dim;
+  swa_dtype dtype;         /* of q and k */
+  swa_dtype grad_dtype;    /* of dq_out and dk_out */
+  swa_dtype out_dtype;     /* of dq and dk */
+  const void* q;
+  const void* k;
+  int64_t q_stride[3], k_stride[3];
+  const int32_t* positions;
+  int start;
+  const void* dq_out;
+  const void* dk_out;
+  int64_t dq_out_stride[3], dk_out_stride[3];
+  void* dq;
+  void* dk;
+  int64_t dq_stride[3], dk_stride[3];
+  float* dq_weight;
+  float* dk_weight;
+  swa_rotation rotation;
+  swa_head_norm head_norm;
+  void* workspace;
+  size_t workspace_bytes;
+} swa_rotary_backward_args;
+
+/* With dtype SWA_FP32, grad_dtype and out_dtype must be SWA_FP32 too.  Statuses as
+ * swa_rotary_forward; SWA_ERR_INVALID_ARG also for a workspace that is too small. */
+swa_status swa_rotary_backward(const swa_rotary_backward_args* args, void* stream);
+size_t swa_rotary_workspace_bytes(const swa_rotary_backward_args* args);
+
+/* ---------------------------------------------------------------------------
+ * Paged key / value cache: decoding with the causal layers ("SWAN-GPT" §3.3(1):
+ * sliding-window layers with a fixed causal window between layers without one).
+ * Pages hold page_size consecutive positions of one sequence for every KV head:
+ *   k_pages, v_pages   [num_pages, Hkv, page_size, D]   contiguous, dtype of the cache
+ * and position t of sequence b lies in page block_table[b][t / page_size].  A page may
+ * belong to several sequences (a shared prefix) as long as no call appends to it for
+ * two of them.
+ *
+ * A call's new tokens are packed: row i of a [T, heads, D] tensor belongs to the
+ * sequence b with cu_tokens[b] <= i < cu_tokens[b + 1], or to b = i / (T / B) when
+ * cu_tokens is NULL.  seq_lens[b] counts the sequence's positions WITH its new
+ * tokens, so its c new tokens lie at positions seq_lens[b] - c, ..., seq_lens[b] - 1.
+ * Rows from cu_tokens[B] on belong to nobody: nothing of theirs is written.
+ *
+ * The device inputs are not checked before the kernels run; what they find wrong
+ * there (a page outside the pool, a position before 0 or beyond the table, cu_tokens
+ * that decrease or pass T, a sequence beyond max_tokens or max_len) reads and writes
+ * nothing out of bounds -- the row or key is left out -- and sets a bit of
+ * *error_word, which swa_cache_check reports as SWA_ERR_DEVICE_CHECK.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* k_pages;           /* device, 16-byte aligned */
+  void* v_pages;
+  int num_pages;           /* >= 1 */
+  int num_kv_heads;        /* >= 1 */
+  int page_size;           /* a multiple of 16 (else SWA_ERR_UNSUPPORTED) */
+  int head_dim;            /* 64 or 128 */
+  swa_dtype dtype;
+  int32_t* error_word;     /* device, zero at first */
+} swa_cache;
+
+typedef struct {
+  int batch;                   /* sequences, >= 0 */
+  int num_tokens;              /* T >= 0: rows of the packed tensors */
+  const int32_t* block_table;  /* device [B, max_pages]; entries of pages no key or row of the
+                                  call touches may hold anything */
+  int max_pages;               /* >= 1 */
+  const int32_t* seq_lens;     /* device [B] */
+  const int32_t* cu_tokens;    /* device [B + 1] starting at 0, or NULL: T / B tokens each */
+} swa_cache_batch;
+
+/* Write the new tokens' keys (normed and rotated at their positions) and values into
+ * the pages, and rotate their queries: one launch on `stream`. */
+typedef struct {
+  int num_q_heads;             /* 0: no queries */
+  const void* q;               /* device [T, Hq, D], strides (token, head); dtype of the cache */
+  const void* k;               /* device [T, Hkv, D] */
+  const void* v;
+  int64_t q_stride[2], k_stride[2], v_stride[2];
+  void* q_out;                 /* device [T, Hq, D], strides (token, head); may be q */
+  int64_t q_out_stride[2];
+  swa_rotation rotation;       /* rotary_dim 0: keys are stored as they come */
+  swa_head_norm head_norm;
+} swa_cache_append_args;
+
+swa_status swa_cache_append(const swa_cache* cache, const swa_cache_batch* batch,
+                            const swa_cache_append_args* args, void* stream);
+
+/* Attention of the new tokens' queries over the cache (which holds their own keys
+ * already): query head h of a token at position t attends, with KV head
+ * h / (Hq / Hkv), the positions max(0, t - window) .. t;
+ *   s = scale <q, k>, then s = softcap * tanh(s / softcap) when softcap > 0;
+ *   out = softmax(s) . V, lse = natural-log logsumexp of s.
+ * A token without a key (all its pages bad) gives out = 0 and lse = -inf.  Values at
+ * positions that no query of the call's sequence attends never reach a result,
+ * whatever they hold (also NaN); a position that some but not all of a sequence's new
+ * tokens attend must hold finite values, or any of that sequence's new tokens may
+ * turn NaN. */
+typedef struct {
+  int num_q_heads;             /* a multiple of the cache's num_kv_heads, <= 128 */
+  const void* q;               /* device [T, Hq, D], strides (token, head) */
+  int64_t q_stride[2];
+  int max_tokens;              /* no sequence has more new tokens (ignored without cu_tokens) */
+  int max_len;                 /* no seq_lens[b] is larger; 0: max_pages * page_size */
+  int window;                  /* one-sided radius >= 0, or -1: no window */
+  float softcap;               /* 0: none */
+  float scale;                 /* 0 selects 1/sqrt(head_dim) */
+  void* out;                   /* device [T, Hq, D] contiguous, 16-byte aligned */
+  float* lse;                  /* device [T, Hq], or NULL */
+  void* workspace;             /* device, 16-byte aligned: partial results of split sequences */
+  size_t workspace_bytes;      /* >= swa_cache_attend_workspace_bytes(...) */
+} swa_cache_attend_args;
+
+swa_status swa_cache_attend(const swa_cache* cache, const swa_cache_batch* batch,
+                            const swa_cache_attend_args* args, void* stream);
+
+/* Device workspace the attend call needs (0: none).  It depends on sizes only, not on
+ * pointers or device contents; the call uses it only until its kernels have run. */
+size_t swa_cache_attend_workspace_bytes(const swa_cache* cache, const swa_cache_batch* batch,
+                                        const swa_cache_attend_args* args);
+
+/* Synchronise `stream`, read the cache's error word and clear it: SWA_OK,
+ * SWA_ERR_DEVICE_CHECK, SWA_ERR_TIMEOUT or SWA_ERR_CUDA. */
+swa_status swa_cache_check(const swa_cache* cache, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

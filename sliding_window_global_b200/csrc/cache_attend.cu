@@ -1,0 +1,406 @@
+// cache_attend.cu -- attention over a paged cache: the entry points, the CUDA-core
+// kernel, and the merge of split sequences.  The definition stands in include/swa.h.
+//
+// A row is one (new token, query head) pair; the rows of a KV head's query heads are
+// packed token by token (row r = token * G + head in the group), so that a key tile is
+// read once for the whole group.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "cache_device.cuh"
+#include "rotary_math.cuh"
+#include "swa_host.h"
+
+namespace swa {
+namespace {
+
+constexpr int kRows = 64, kKeys = 64;      // tile of the CUDA-core kernel
+constexpr int kCoreThreads = 256;
+
+template <int D>
+constexpr int core_smem_bytes() {
+  return (kRows * (D + 4) + kKeys * (D + 4) + kRows * (kKeys + 4)) * 4 + kKeys * 4;
+}
+
+// 64 rows x 64 keys a step in fp32 on the FMA pipe, each thread 4 x 4 scores and
+// 4 x D/16 outputs; K and V take turns in one shared buffer so that two blocks fit on
+// an SM and one computes while the other loads.
+template <typename T, int D>
+__global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_constant__ CacheAttendParams p,
+                                                                  int row_tiles) {
+  constexpr int LD = D + 4, LP = kKeys + 4;
+  constexpr int NC = D / 64;               // float4 columns of a thread
+  extern __shared__ float smem[];
+  float* sQ = smem;
+  float* sKV = sQ + kRows * LD;
+  float* sP = sKV + kKeys * LD;
+  int* sOk = reinterpret_cast<int*>(sP + kRows * LP);
+
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int hk = blockIdx.y;
+  const int split = blockIdx.x % p.nsplit;
+  const int rt = blockIdx.x / p.nsplit % row_tiles;
+  const int b = blockIdx.x / p.nsplit / row_tiles;
+  const CacheSeq s = cache_seq(p, b);
+  if (s.bad && tid == 0 && rt == 0 && split == 0 && hk == 0) atomicOr(p.err, kDevErrCheck);
+  const int rows = s.count * p.G;
+  const int r0 = rt * kRows;
+  if (r0 >= rows) return;
+
+  // Q rows (zeros behind the last one)
+  for (int e = tid; e < kRows * (D / 8); e += kCoreThreads) {
+    const int r = e / (D / 8), c = e % (D / 8) * 8;
+    float x[8];
+    if (r0 + r < rows) {
+      const int tok = (r0 + r) / p.G, h = hk * p.G + (r0 + r) % p.G;
+      unpack(load_chunk(static_cast<const T*>(p.q) + (long long)(s.from + tok) * p.q_token + h * p.q_head + c), x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sQ[r * LD + c + i] = x[i];
+  }
+
+  const int t0 = r0 / p.G, t1 = min((r0 + kRows - 1) / p.G, s.count - 1);
+  int lo = key_begin(p, s, t0);
+  const int hi = key_end(s, t1);
+  const int tiles = hi > lo ? (hi - lo + kKeys - 1) / kKeys : 0;
+  const int j0 = (int)((long long)tiles * split / p.nsplit), j1 = (int)((long long)tiles * (split + 1) / p.nsplit);
+
+  int klo[4], khi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + ty * 4 + i;
+    klo[i] = r < rows ? key_begin(p, s, r / p.G) : 0;
+    khi[i] = r < rows ? key_end(s, r / p.G) : 0;
+  }
+  float m[4], l[4], o[4][4 * NC];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
+  }
+
+  for (int j = j0; j < j1; ++j) {
+    const int key0 = lo + j * kKeys;
+    // a key exists if it lies in the tile's range and its page in the pool
+    auto load = [&](const void* pages, bool keys) {
+      for (int e = tid; e < kKeys * (D / 8); e += kCoreThreads) {
+        const int k = e / (D / 8), c = e % (D / 8) * 8;
+        const int pos = key0 + k;
+        float x[8];
+        bool ok = pos < hi;
+        if (ok) {
+          const int page = __ldg(p.block_table + (long long)b * p.max_pages + pos / p.page_size);
+          ok = page >= 0 && page < p.num_pages;
+          if (ok)
+            unpack(load_chunk(static_cast<const T*>(pages) +
+                              (((long long)page * p.Hkv + hk) * p.page_size + pos % p.page_size) * D + c), x);
+          else if (keys && c == 0) atomicOr(p.err, kDevErrCheck);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sKV[k * LD + c + i] = ok ? x[i] : 0.f;
+        if (keys && c == 0) sOk[k] = ok;
+      }
+    };
+    __syncthreads();                       // the previous step's V has been read
+    load(p.k_pages, true);
+    __syncthreads();
+    float sc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sc[i][k] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+      float4 q4[4], k4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q4[i] = *reinterpret_cast<const float4*>(sQ + (ty * 4 + i) * LD + d);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) k4[k] = *reinterpret_cast<const float4*>(sKV + (tx + 16 * k) * LD + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sc[i][k] += q4[i].x * k4[k].x + q4[i].y * k4[k].y + q4[i].z * k4[k].z + q4[i].w * k4[k].w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = m[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int pos = key0 + tx + 16 * k;
+        float x = sc[i][k] * p.scale;
+        if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
+        sc[i][k] = (pos >= klo[i] && pos < khi[i] && sOk[tx + 16 * k]) ? x : -INFINITY;
+        mx = fmaxf(mx, sc[i][k]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      const float alpha = m[i] == -INFINITY ? 0.f : expf(m[i] - ref);
+      m[i] = mx;
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float e = expf(sc[i][k] - ref);
+        sP[(ty * 4 + i) * LP + tx + 16 * k] = e;
+        sum += e;
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l[i] = l[i] * alpha + sum;
+#pragma unroll
+      for (int c = 0; c < 4 * NC; ++c) o[i][c] *= alpha;
+    }
+    __syncthreads();                       // K has been read, P is written
+    load(p.v_pages, false);
+    __syncthreads();
+#pragma unroll 4
+    for (int k = 0; k < kKeys; k += 4) {
+      float4 pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4*>(sP + (ty * 4 + i) * LP + k);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(sKV + (k + kk) * LD + tx * 4 + 64 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
+            o[i][4 * c] += w * v.x;
+            o[i][4 * c + 1] += w * v.y;
+            o[i][4 * c + 2] += w * v.z;
+            o[i][4 * c + 3] += w * v.w;
+          }
+        }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + ty * 4 + i;
+    if (r >= rows) continue;
+    const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
+    const bool has = m[i] != -INFINITY;
+    const float inv = has ? 1.f / l[i] : 0.f;
+    const float lse = has ? m[i] + logf(l[i]) : -INFINITY;
+    if (p.nsplit > 1) {
+      const long long pr = (long long)split * p.T * p.Hq + row;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        *reinterpret_cast<float4*>(p.part_o + pr * D + tx * 4 + 64 * c) =
+            make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
+      if (tx == 0) p.part_lse[pr] = lse;
+    } else {
+      T* out = static_cast<T*>(p.out) + row * D;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[tx * 4 + 64 * c + e] = static_cast<T>(o[i][4 * c + e] * inv);
+      if (p.lse && tx == 0) p.lse[row] = lse;
+    }
+  }
+}
+
+// out = sum_s exp(lse_s - lse) out_s over the splits in order, lse = log sum_s exp(lse_s):
+// one warp a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant__ CacheAttendParams p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int h = (int)(id % p.Hq);
+  const int i = (int)(id / p.Hq % p.max_tokens);
+  const long long b = id / p.Hq / p.max_tokens;
+  if (b >= p.B) return;
+  const CacheSeq s = cache_seq(p, (int)b);
+  if (i >= s.count) return;
+  const long long row = (long long)(s.from + i) * p.Hq + h, step = (long long)p.T * p.Hq;
+  float top = -INFINITY;
+  for (int k = 0; k < p.nsplit; ++k) top = fmaxf(top, p.part_lse[k * step + row]);
+  float acc[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int k = 0; k < p.nsplit; ++k) {
+    const float w = p.part_lse[k * step + row];
+    if (w == -INFINITY) continue;          // a split without keys (NaN goes on)
+    const float f = expf(w - top);
+    sum += f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += f * p.part_o[(k * step + row) * D + lane * E + e];
+  }
+  const bool has = sum != 0.f;
+  const float inv = has ? 1.f / sum : 0.f;
+  T* out = static_cast<T*>(p.out) + row * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = static_cast<T>(acc[e] * inv);
+  if (p.lse && lane == 0) p.lse[row] = has ? top + logf(sum) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ launches
+template <typename T, int D>
+cudaError_t launch_core(const CacheAttendParams& p, int row_tiles, cudaStream_t s) {
+  auto kern = cache_core_kernel<T, D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, core_smem_bytes<D>());
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((unsigned)((long long)p.B * row_tiles * p.nsplit), p.Hkv), kCoreThreads, core_smem_bytes<D>(), s>>>(
+      p, row_tiles);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_merge(const CacheAttendParams& p, cudaStream_t s) {
+  const long long rows = (long long)p.B * p.max_tokens * p.Hq;
+  const unsigned blocks = (unsigned)((rows + 3) / 4);
+  if (p.D == 64) cache_merge_kernel<T, 64><<<blocks, 128, 0, s>>>(p);
+  else cache_merge_kernel<T, 128><<<blocks, 128, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// How a call is cut up: rows a tile, parts of a sequence's keys.  Sizes only.
+struct AttendSplit {
+  int row_tiles, nsplit;
+};
+
+AttendSplit attend_split(const swa_cache& c, const swa_cache_batch& b, const swa_cache_attend_args& a, int max_tokens,
+                         int max_len) {
+  AttendSplit r;
+  const int G = a.num_q_heads / c.num_kv_heads;
+  r.row_tiles = (int)(((long long)max_tokens * G + kRows - 1) / kRows);
+  // keys a tile of rows can reach; parts of at least 256, two blocks an SM
+  const long long reach = a.window < 0 ? max_len : std::min<long long>(max_len, (long long)a.window + max_tokens);
+  const long long blocks = (long long)b.batch * r.row_tiles * c.num_kv_heads;
+  const long long want = (148 * 2 + blocks - 1) / std::max<long long>(blocks, 1);
+  r.nsplit = (int)std::max<long long>(1, std::min<long long>({want, reach / 256, 64}));
+  return r;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes of an attend call, checked: the status, and the bounds the kernels use.
+swa_status attend_bounds(const swa_cache& c, const swa_cache_batch& b, const swa_cache_attend_args& a, int* max_tokens,
+                         int* max_len) {
+  swa_status st = check_cache(c);
+  if (st == SWA_OK) st = check_batch(b);
+  if (st != SWA_OK) return st;
+  if (a.num_q_heads < 1 || a.num_q_heads % c.num_kv_heads != 0 || a.window < -1 || a.max_len < 0 ||
+      !(a.softcap >= 0.f) || !isfinite(a.softcap) || !(a.scale >= 0.f) || !isfinite(a.scale) ||
+      (b.cu_tokens && a.max_tokens < 0))
+    return SWA_ERR_INVALID_ARG;
+  if (a.num_q_heads > kMaxHeads) return SWA_ERR_UNSUPPORTED;
+  const long long capacity = (long long)b.max_pages * c.page_size;
+  *max_tokens = b.cu_tokens ? std::min(a.max_tokens, b.num_tokens) : (b.batch ? b.num_tokens / b.batch : 0);
+  *max_len = (int)std::min<long long>(a.max_len ? a.max_len : capacity, capacity);
+  if ((long long)b.batch * *max_tokens * a.num_q_heads > 0x7fffffffLL ||
+      (long long)b.num_tokens * a.num_q_heads > 0x7fffffffLL)
+    return SWA_ERR_UNSUPPORTED;
+  return SWA_OK;
+}
+
+}  // namespace
+
+swa_status check_cache(const swa_cache& c) {
+  if (!c.k_pages || !c.v_pages || !c.error_word || !aligned16(c.k_pages) || !aligned16(c.v_pages) ||
+      !aligned4(c.error_word) || c.num_pages < 1 || c.num_kv_heads < 1 || c.page_size < 1 || c.head_dim < 1 ||
+      (c.dtype != SWA_BF16 && c.dtype != SWA_FP32))
+    return SWA_ERR_INVALID_ARG;
+  if ((c.head_dim != 64 && c.head_dim != 128) || c.page_size % 16 != 0 || c.num_kv_heads > kMaxHeads ||
+      (long long)c.num_pages * c.num_kv_heads > 0x7fffffffLL)
+    return SWA_ERR_UNSUPPORTED;
+  return SWA_OK;
+}
+
+swa_status check_batch(const swa_cache_batch& b) {
+  if (b.batch < 0 || b.num_tokens < 0 || b.max_pages < 1) return SWA_ERR_INVALID_ARG;
+  if (b.batch > 0 && b.num_tokens > 0 &&
+      (!b.block_table || !b.seq_lens || !aligned4(b.block_table) || !aligned4(b.seq_lens) || !aligned4(b.cu_tokens) ||
+       (!b.cu_tokens && b.num_tokens % b.batch != 0)))
+    return SWA_ERR_INVALID_ARG;
+  if (b.num_tokens > 0x7fffffff - 64) return SWA_ERR_UNSUPPORTED;
+  return SWA_OK;
+}
+
+}  // namespace swa
+
+extern "C" {
+
+size_t swa_cache_attend_workspace_bytes(const swa_cache* c, const swa_cache_batch* b, const swa_cache_attend_args* a) {
+  int max_tokens, max_len;
+  if (!c || !b || !a || swa::attend_bounds(*c, *b, *a, &max_tokens, &max_len) != SWA_OK) return 0;
+  if (b->batch == 0 || b->num_tokens == 0 || max_tokens == 0) return 0;
+  const swa::AttendSplit sp = swa::attend_split(*c, *b, *a, max_tokens, max_len);
+  if (sp.nsplit == 1) return 0;
+  return (size_t)sp.nsplit * b->num_tokens * a->num_q_heads * (c->head_dim + 1) * 4;
+}
+
+swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const swa_cache_attend_args* a,
+                            void* stream) {
+  if (!c || !b || !a) return SWA_ERR_INVALID_ARG;
+  swa::CacheAttendParams p = {};
+  const swa_status st = swa::attend_bounds(*c, *b, *a, &p.max_tokens, &p.max_len);
+  if (st != SWA_OK) return st;
+  if (b->batch == 0 || b->num_tokens == 0 || p.max_tokens == 0) return SWA_OK;
+  const int64_t unit = c->dtype == SWA_FP32 ? 4 : 8;
+  if (!a->q || !a->out || !swa::aligned16(a->q) || !swa::aligned16(a->out) || !swa::aligned4(a->lse) ||
+      (b->num_tokens > 1 && (a->q_stride[0] < 0 || a->q_stride[0] % unit)) ||
+      (a->num_q_heads > 1 && (a->q_stride[1] < 0 || a->q_stride[1] % unit)))
+    return SWA_ERR_INVALID_ARG;
+  const swa::AttendSplit sp = swa::attend_split(*c, *b, *a, p.max_tokens, p.max_len);
+  p.k_pages = c->k_pages;
+  p.v_pages = c->v_pages;
+  p.q = a->q;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.block_table = b->block_table;
+  p.seq_lens = b->seq_lens;
+  p.cu_tokens = b->cu_tokens;
+  p.err = c->error_word;
+  p.q_token = a->q_stride[0];
+  p.q_head = a->q_stride[1];
+  p.B = b->batch;
+  p.T = b->num_tokens;
+  p.Hq = a->num_q_heads;
+  p.Hkv = c->num_kv_heads;
+  p.G = p.Hq / p.Hkv;
+  p.D = c->head_dim;
+  p.num_pages = c->num_pages;
+  p.page_size = c->page_size;
+  p.max_pages = b->max_pages;
+  p.window = a->window;
+  p.nsplit = sp.nsplit;
+  p.scale = a->scale == 0.f ? 1.f / sqrtf((float)p.D) : a->scale;
+  p.softcap = a->softcap;
+  if (p.nsplit > 1) {
+    const size_t rows = (size_t)p.nsplit * p.T * p.Hq;
+    if (!a->workspace || !swa::aligned16(a->workspace) || a->workspace_bytes < rows * (p.D + 1) * 4)
+      return SWA_ERR_INVALID_ARG;
+    p.part_o = static_cast<float*>(a->workspace);
+    p.part_lse = p.part_o + rows * p.D;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (c->dtype == SWA_FP32)
+    e = p.D == 64 ? swa::launch_core<float, 64>(p, sp.row_tiles, s) : swa::launch_core<float, 128>(p, sp.row_tiles, s);
+  else
+    e = p.D == 64 ? swa::launch_core<__nv_bfloat16, 64>(p, sp.row_tiles, s)
+                  : swa::launch_core<__nv_bfloat16, 128>(p, sp.row_tiles, s);
+  if (e == cudaSuccess && p.nsplit > 1)
+    e = c->dtype == SWA_FP32 ? swa::launch_merge<float>(p, s) : swa::launch_merge<__nv_bfloat16>(p, s);
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+swa_status swa_cache_check(const swa_cache* c, void* stream) {
+  if (!c || !c->error_word || !swa::aligned4(c->error_word)) return SWA_ERR_INVALID_ARG;
+  return swa::read_and_clear_error(c->error_word, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

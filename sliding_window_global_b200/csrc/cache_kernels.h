@@ -1,0 +1,38 @@
+// cache_kernels.h -- checks, parameter block and launchers of the attention over a paged
+// cache.  Internal to the library.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/swa.h"
+
+namespace swa {
+
+// Checks of a cache and of a batch: SWA_ERR_INVALID_ARG for a null or misaligned pointer
+// or a bad size, SWA_ERR_UNSUPPORTED for a shape the kernels do not implement.
+swa_status check_cache(const swa_cache& c);
+swa_status check_batch(const swa_cache_batch& b);
+
+struct CacheAttendParams {
+  const void* k_pages;
+  const void* v_pages;
+  const void* q;
+  void* out;                        // [T, Hq, D]
+  float* lse;                       // [T, Hq] or null
+  const int32_t* block_table;       // [B, max_pages]
+  const int32_t* seq_lens;          // [B]
+  const int32_t* cu_tokens;         // [B + 1] or null
+  int* err;
+  float* part_o;                    // [nsplit, T, Hq, D] unnormalised nowhere: each split's own softmax
+  float* part_lse;                  // [nsplit, T, Hq]
+  long long q_token, q_head;        // strides of q, elements
+  int B, T, Hq, Hkv, G, D;
+  int num_pages, page_size, max_pages;
+  int max_tokens, max_len;          // bounds on a sequence's new tokens and length
+  int window;                       // < 0: none
+  int nsplit;                       // parts of a sequence's keys
+  float scale, softcap;
+};
+
+}  // namespace swa

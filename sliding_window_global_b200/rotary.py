@@ -1,0 +1,311 @@
+"""ctypes binding of the rotation and head norm (swa_rotary_forward / _backward).
+
+Argument marshalling only, as in ``swa.py``: the arithmetic runs in the library's CUDA
+kernels, and a call on anything but CUDA tensors raises.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from .swa import SwaError, _dtype_code, load_library
+
+P, I, I64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+
+
+class Rotation(ctypes.Structure):
+    """swa_rotation of include/swa.h."""
+    _fields_ = [("rotary_dim", I), ("interleaved", I), ("freq", P), ("amplitude", F)]
+
+
+class HeadNorm(ctypes.Structure):
+    """swa_head_norm of include/swa.h."""
+    _fields_ = [("norm", I), ("eps", F), ("q_weight", P), ("k_weight", P), ("weight_dtype", I)]
+
+
+class RotaryArgs(ctypes.Structure):
+    """swa_rotary_args of include/swa.h (each stride array as its elements)."""
+    _fields_ = [
+        ("batch", I), ("seq_len", I), ("num_q_heads", I), ("num_kv_heads", I), ("head_dim", I), ("dtype", I),
+        ("q", P), ("k", P),
+        ("q_stride0", I64), ("q_stride1", I64), ("q_stride2", I64),
+        ("k_stride0", I64), ("k_stride1", I64), ("k_stride2", I64),
+        ("positions", P), ("start", I), ("q_out", P), ("k_out", P),
+        ("q_out_stride0", I64), ("q_out_stride1", I64), ("q_out_stride2", I64),
+        ("k_out_stride0", I64), ("k_out_stride1", I64), ("k_out_stride2", I64),
+        ("rotation", Rotation), ("head_norm", HeadNorm),
+    ]
+
+
+class RotaryBackwardArgs(ctypes.Structure):
+    """swa_rotary_backward_args of include/swa.h (each stride array as its elements)."""
+    _fields_ = [
+        ("batch", I), ("seq_len", I), ("num_q_heads", I), ("num_kv_heads", I), ("head_dim", I),
+        ("dtype", I), ("grad_dtype", I), ("out_dtype", I), ("q", P), ("k", P),
+        ("q_stride0", I64), ("q_stride1", I64), ("q_stride2", I64),
+        ("k_stride0", I64), ("k_stride1", I64), ("k_stride2", I64),
+        ("positions", P), ("start", I), ("dq_out", P), ("dk_out", P),
+        ("dq_out_stride0", I64), ("dq_out_stride1", I64), ("dq_out_stride2", I64),
+        ("dk_out_stride0", I64), ("dk_out_stride1", I64), ("dk_out_stride2", I64),
+        ("dq", P), ("dk", P),
+        ("dq_stride0", I64), ("dq_stride1", I64), ("dq_stride2", I64),
+        ("dk_stride0", I64), ("dk_stride1", I64), ("dk_stride2", I64),
+        ("dq_weight", P), ("dk_weight", P), ("rotation", Rotation), ("head_norm", HeadNorm),
+        ("workspace", P), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+NO_STRIDES = (0, 0, 0)
+_NO_ROTATION = Rotation(0, 0, None, 1.0)
+_NO_NORM = HeadNorm(0, 0.0, None, None, 0)
+
+
+def on_device(t: torch.Tensor, stream):
+    """Context in which a call on ``t`` runs: its device current, and ``stream`` (when
+    given) the one that outputs and workspaces are allocated for."""
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.get_device() != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def current_stream() -> ctypes.c_void_p:
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def check_rows(t: torch.Tensor, name: str, like: torch.Tensor, dims: int, dtype=None):
+    """A tensor of head rows: on the device of ``like``, ``dims`` axes, the last one dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} needs {dims} axes, got {t.dim()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.stride(-1) != 1 and t.numel() > 0:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+
+
+def check_index(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape):
+    """An int32 tensor of the given shape (or None); returns its address."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def head_norm(norm_eps, q_weight, k_weight, head_dim: int, like: torch.Tensor) -> HeadNorm:
+    """swa_head_norm of the arguments (norm_eps None: no norm)."""
+    if norm_eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("norm weights need norm_eps")
+        return _NO_NORM
+    code, ptrs = 0, []
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            ptrs.append(None)
+            continue
+        check_rows(w, name, like, 1)
+        if w.shape[0] != head_dim:
+            raise ValueError(f"{name} must have {head_dim} elements, got {w.shape[0]}")
+        ptrs.append(w.data_ptr())
+        code = _dtype_code(w.dtype)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must have one dtype")
+    return HeadNorm(1, float(norm_eps), ptrs[0], ptrs[1], code)
+
+
+def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original_length: int = 4096, low_turns: float = 1.0, high_turns: float = 32.0):
+    """Radians a position for each of the ``rotary_dim / 2`` pairs (fp64, on the host), and
+    the amplitude: ``freq[j] = base ** (-2 j / rotary_dim)``, stretched for contexts
+    ``factor`` times the trained length:
+
+    - ``"linear"``: every frequency divided by the factor (positions interpolated);
+    - ``"ntk"``: the base grows by ``factor ** (rotary_dim / (rotary_dim - 2))``, so that the
+      slowest pair is interpolated and the fastest kept;
+    - ``"yarn"``: pairs that turn more than ``high_turns`` times over ``original_length`` are
+      kept, those below ``low_turns`` interpolated, a linear ramp between, and the rotated
+      vectors scaled by ``0.1 ln(factor) + 1``."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not factor > 0.0 or not base > 0.0:
+        raise ValueError("base and factor must be positive")
+    j = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rotary_dim < 4:
+            raise ValueError("ntk scaling needs a rotary_dim of 4 or more")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    freq = base ** (-2.0 * j / rotary_dim)
+    if scaling in ("none", "ntk"):
+        return freq, 1.0
+    if scaling == "linear":
+        return freq / factor, 1.0
+    if scaling == "yarn":
+        turns = original_length * freq / (2.0 * math.pi)
+        keep = ((turns - low_turns) / (high_turns - low_turns)).clamp(0.0, 1.0)
+        return freq * keep + freq / factor * (1.0 - keep), 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"unknown scaling {scaling!r}; use none, linear, ntk or yarn")
+
+
+class Rotary:
+    """Rotation of query and key heads by their positions, with an optional RMS norm of
+    every head before it, and its gradients.
+
+    ``rotary_dim`` leading elements of a head rotate (all by default), in pairs
+    ``(2j, 2j + 1)`` (``interleaved``) or ``(j, j + rotary_dim / 2)``; ``frequencies`` gives
+    the radians a position of each pair (``rotary_frequencies`` makes them; base 10000
+    without scaling by default), ``amplitude`` scales the rotated elements."""
+
+    def __init__(self, head_dim: int, *, rotary_dim: Optional[int] = None, interleaved: bool = True,
+                 frequencies: Optional[torch.Tensor] = None, amplitude: float = 1.0):
+        self._lib = load_library()
+        self.head_dim = int(head_dim)
+        self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
+        self.interleaved = bool(interleaved)
+        self.amplitude = float(amplitude)
+        if head_dim not in (64, 128) or self.rotary_dim % 16 or not 0 <= self.rotary_dim <= self.head_dim:
+            raise ValueError("head_dim must be 64 or 128 and rotary_dim a multiple of 16 up to it, "
+                             f"got {head_dim} and {self.rotary_dim}")
+        if not math.isfinite(self.amplitude) or self.amplitude == 0.0:
+            raise ValueError("amplitude must be finite and not zero")
+        if frequencies is None:
+            frequencies = rotary_frequencies(self.rotary_dim)[0] if self.rotary_dim else torch.empty(0)
+        freq = frequencies.detach().to("cpu", torch.float64).reshape(-1).tolist()
+        if len(freq) != self.rotary_dim // 2 or not all(math.isfinite(f) for f in freq):
+            raise ValueError(f"frequencies needs {self.rotary_dim // 2} finite values")
+        self._freq = (ctypes.c_double * max(1, len(freq)))(*freq)
+        self.struct = Rotation(self.rotary_dim, int(self.interleaved), ctypes.addressof(self._freq), self.amplitude)
+
+    def forward(self, q: torch.Tensor, k: Optional[torch.Tensor] = None, *, positions: Optional[torch.Tensor] = None,
+                start: int = 0, norm_eps: Optional[float] = None, q_weight: Optional[torch.Tensor] = None,
+                k_weight: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                k_out: Optional[torch.Tensor] = None, stream=None):
+        """Rotated q [B, Hq, n, D] and k [B, Hkv, n, D] (any strides with a dense last axis, so
+        a slice of a projection's output as it lies); ``positions`` int32 [B, n], or ``start``,
+        ``start + 1``, ... in every batch.  ``norm_eps``: norm every head first, times the
+        weights [D].  Outputs are contiguous unless given; an output may be its input.
+        Returns ``(q_out, k_out)``."""
+        check_rows(q, "q", q, 4)
+        B, Hq, n, D = q.shape
+        dtype = _dtype_code(q.dtype)
+        if D != self.head_dim:
+            raise ValueError(f"q has head_dim {D}, expected {self.head_dim}")
+        Hkv = 0
+        if k is not None:
+            check_rows(k, "k", q, 4, q.dtype)
+            Hkv = k.shape[1]
+            if k.shape[0] != B or k.shape[2] != n or k.shape[3] != D:
+                raise ValueError(f"k must be [{B}, heads, {n}, {D}], got {tuple(k.shape)}")
+        with on_device(q, stream):
+            if q_out is None:
+                q_out = torch.empty((B, Hq, n, D), dtype=q.dtype, device=q.device)
+            else:
+                self._check_out(q_out, "q_out", q)
+            if k is None:
+                k_out = None
+            elif k_out is None:
+                k_out = torch.empty((B, Hkv, n, D), dtype=q.dtype, device=q.device)
+            else:
+                self._check_out(k_out, "k_out", k)
+            qs, os = q.stride(), q_out.stride()
+            ks, kos = (NO_STRIDES, NO_STRIDES) if k is None else (k.stride(), k_out.stride())
+            a = RotaryArgs(
+                B, n, Hq, Hkv, D, dtype, q.data_ptr(), None if k is None else k.data_ptr(), qs[0], qs[1], qs[2],
+                ks[0], ks[1], ks[2], check_index(positions, "positions", q, (B, n)), int(start), q_out.data_ptr(),
+                None if k is None else k_out.data_ptr(), os[0], os[1], os[2], kos[0], kos[1], kos[2], self.struct,
+                head_norm(norm_eps, q_weight, k_weight, D, q))
+            st = self._lib.swa_rotary_forward(ctypes.byref(a), current_stream())
+        if st != 0:
+            raise SwaError(st, "swa_rotary_forward")
+        return q_out, k_out
+
+    def backward(self, dq_out: torch.Tensor, dk_out: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                 k: Optional[torch.Tensor] = None, *, positions: Optional[torch.Tensor] = None, start: int = 0,
+                 norm_eps: Optional[float] = None, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, dq: Optional[torch.Tensor] = None,
+                 dk: Optional[torch.Tensor] = None, stream=None):
+        """Gradients for the upstream ``dq_out``, ``dk_out`` (as ``Plan.backward`` gives them, or
+        bf16).  ``q``, ``k`` are the forward's inputs, required with a norm; they set the
+        gradients' dtype and layout (without them, the upstream's).  Returns ``(dq, dk)``, and
+        with a norm ``(dq, dk, dq_weight, dk_weight)`` (fp32 [D]; None without that weight)."""
+        check_rows(dq_out, "dq_out", dq_out, 4)
+        B, Hq, n, D = dq_out.shape
+        if D != self.head_dim:
+            raise ValueError(f"dq_out has head_dim {D}, expected {self.head_dim}")
+        Hkv = 0
+        if dk_out is not None:
+            check_rows(dk_out, "dk_out", dq_out, 4, dq_out.dtype)
+            Hkv = dk_out.shape[1]
+            if dk_out.shape[0] != B or dk_out.shape[2] != n or dk_out.shape[3] != D:
+                raise ValueError(f"dk_out must be [{B}, heads, {n}, {D}], got {tuple(dk_out.shape)}")
+        if norm_eps is not None and (q is None or (k is None and Hkv > 0)):
+            raise ValueError("the norm's gradient needs q and k")
+        for name, x, g in (("q", q, dq_out), ("k", k, dk_out)):
+            if x is None:
+                continue
+            if g is None:
+                raise ValueError(f"{name} without d{name}_out")
+            check_rows(x, name, dq_out, 4, None if q is None else q.dtype)
+            if x.shape != g.shape:
+                raise ValueError(f"{name} must have shape {tuple(g.shape)}, got {tuple(x.shape)}")
+        with on_device(dq_out, stream):
+            hn = head_norm(norm_eps, q_weight, k_weight, D, dq_out)
+            x_like = q if q is not None else (k if k is not None else dq_out)
+            if dq is None:
+                dq = torch.empty_like(q if q is not None else dq_out, dtype=x_like.dtype)
+            else:
+                self._check_out(dq, "dq", dq_out, dtype=None)
+            if dk_out is None:
+                dk = None
+            elif dk is None:
+                dk = torch.empty_like(k if k is not None else dk_out, dtype=dq.dtype)
+            else:
+                self._check_out(dk, "dk", dk_out, dtype=dq.dtype)
+            dqw = dkw = None
+            if q_weight is not None:
+                dqw = torch.empty(D, dtype=torch.float32, device=dq_out.device)
+            if k_weight is not None and Hkv > 0:
+                dkw = torch.empty(D, dtype=torch.float32, device=dq_out.device)
+            has_k = dk_out is not None
+            qs = NO_STRIDES if q is None else q.stride()
+            ks = NO_STRIDES if k is None else k.stride()
+            gs, os = dq_out.stride(), dq.stride()
+            gks, oks = (dk_out.stride(), dk.stride()) if has_k else (NO_STRIDES, NO_STRIDES)
+            a = RotaryBackwardArgs(
+                B, n, Hq, Hkv, D, _dtype_code(x_like.dtype), _dtype_code(dq_out.dtype), _dtype_code(dq.dtype),
+                None if q is None else q.data_ptr(), None if k is None else k.data_ptr(), qs[0], qs[1], qs[2],
+                ks[0], ks[1], ks[2], check_index(positions, "positions", dq_out, (B, n)), int(start),
+                dq_out.data_ptr(), dk_out.data_ptr() if has_k else None, gs[0], gs[1], gs[2], gks[0], gks[1], gks[2],
+                dq.data_ptr(), dk.data_ptr() if has_k else None, os[0], os[1], os[2], oks[0], oks[1], oks[2],
+                None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(), self.struct, hn,
+                None, 0)
+            if dqw is not None or dkw is not None:
+                need = self._lib.swa_rotary_workspace_bytes(ctypes.byref(a))
+                ws = torch.empty(need, dtype=torch.uint8, device=dq_out.device)
+                a.workspace, a.workspace_bytes = ws.data_ptr(), need
+            st = self._lib.swa_rotary_backward(ctypes.byref(a), current_stream())
+        if st != 0:
+            raise SwaError(st, "swa_rotary_backward")
+        return (dq, dk) if norm_eps is None else (dq, dk, dqw, dkw)
+
+    @staticmethod
+    def _check_out(t, name, like, dtype=0):
+        check_rows(t, name, like, like.dim(), like.dtype if dtype == 0 else dtype)
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")

@@ -31,7 +31,8 @@ EXPORTS = (
     "swa_plan_workspace_bytes", "swa_plan_last_launches", "swa_status_string",
     "swa_side_aggregate", "swa_relative_bucket", "swa_expand_side_bias", "swa_forward_noalloc",
     "swa_forward_ex", "swa_bucket_local_bias", "swa_backward", "swa_selftest_wait_timeout",
-    "swa_selftest_exp2_poly",
+    "swa_selftest_exp2_poly", "swa_rotary_forward", "swa_rotary_backward", "swa_rotary_workspace_bytes",
+    "swa_cache_append", "swa_cache_attend", "swa_cache_attend_workspace_bytes", "swa_cache_check",
 )
 
 
@@ -127,6 +128,20 @@ def load_library():
         lib.swa_selftest_wait_timeout.restype = I
         lib.swa_selftest_exp2_poly.argtypes = [P, P, I, P]
         lib.swa_selftest_exp2_poly.restype = I
+        lib.swa_rotary_forward.argtypes = [P, P]
+        lib.swa_rotary_forward.restype = I
+        lib.swa_rotary_backward.argtypes = [P, P]
+        lib.swa_rotary_backward.restype = I
+        lib.swa_rotary_workspace_bytes.argtypes = [P]
+        lib.swa_rotary_workspace_bytes.restype = U64
+        lib.swa_cache_append.argtypes = [P, P, P, P]
+        lib.swa_cache_append.restype = I
+        lib.swa_cache_attend.argtypes = [P, P, P, P]
+        lib.swa_cache_attend.restype = I
+        lib.swa_cache_attend_workspace_bytes.argtypes = [P, P, P]
+        lib.swa_cache_attend_workspace_bytes.restype = U64
+        lib.swa_cache_check.argtypes = [P, P]
+        lib.swa_cache_check.restype = I
         _lib = lib
         return lib
 
