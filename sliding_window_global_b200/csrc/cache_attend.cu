@@ -265,21 +265,32 @@ cudaError_t launch_merge(const CacheAttendParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// How a call is cut up: rows a tile, parts of a sequence's keys.  Sizes only.
+// How a call is cut up, from sizes only: which kernel, and its parts.
 struct AttendSplit {
-  int row_tiles, nsplit;
+  bool token;                              // the few-token kernel
+  TokenSplit t;
+  int row_tiles, nsplit;                   // CUDA-core kernel: tiles of rows, parts of the keys
+  size_t bytes;                            // workspace
 };
 
 AttendSplit attend_split(const swa_cache& c, const swa_cache_batch& b, const swa_cache_attend_args& a, int max_tokens,
                          int max_len) {
-  AttendSplit r;
+  AttendSplit r = {};
   const int G = a.num_q_heads / c.num_kv_heads;
-  r.row_tiles = (int)(((long long)max_tokens * G + kRows - 1) / kRows);
-  // keys a tile of rows can reach; parts of at least 256, two blocks an SM
+  // keys a sequence's new tokens can reach
   const long long reach = a.window < 0 ? max_len : std::min<long long>(max_len, (long long)a.window + max_tokens);
+  if (c.dtype == SWA_BF16 && (long long)max_tokens * G <= kTokenRows) {
+    r.token = true;
+    r.t = token_split(b.batch, c.num_kv_heads, c.head_dim, max_tokens * G, reach);
+    r.bytes = r.t.bytes;
+    return r;
+  }
+  r.row_tiles = (int)(((long long)max_tokens * G + kRows - 1) / kRows);
+  // parts of at least 256 keys, two blocks an SM
   const long long blocks = (long long)b.batch * r.row_tiles * c.num_kv_heads;
   const long long want = (148 * 2 + blocks - 1) / std::max<long long>(blocks, 1);
   r.nsplit = (int)std::max<long long>(1, std::min<long long>({want, reach / 256, 64}));
+  if (r.nsplit > 1) r.bytes = (size_t)r.nsplit * b.num_tokens * a.num_q_heads * (c.head_dim + 1) * 4;
   return r;
 }
 
@@ -337,9 +348,7 @@ size_t swa_cache_attend_workspace_bytes(const swa_cache* c, const swa_cache_batc
   int max_tokens, max_len;
   if (!c || !b || !a || swa::attend_bounds(*c, *b, *a, &max_tokens, &max_len) != SWA_OK) return 0;
   if (b->batch == 0 || b->num_tokens == 0 || max_tokens == 0) return 0;
-  const swa::AttendSplit sp = swa::attend_split(*c, *b, *a, max_tokens, max_len);
-  if (sp.nsplit == 1) return 0;
-  return (size_t)sp.nsplit * b->num_tokens * a->num_q_heads * (c->head_dim + 1) * 4;
+  return swa::attend_split(*c, *b, *a, max_tokens, max_len).bytes;
 }
 
 swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const swa_cache_attend_args* a,
@@ -379,15 +388,18 @@ swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const 
   p.nsplit = sp.nsplit;
   p.scale = a->scale == 0.f ? 1.f / sqrtf((float)p.D) : a->scale;
   p.softcap = a->softcap;
-  if (p.nsplit > 1) {
-    const size_t rows = (size_t)p.nsplit * p.T * p.Hq;
-    if (!a->workspace || !swa::aligned16(a->workspace) || a->workspace_bytes < rows * (p.D + 1) * 4)
-      return SWA_ERR_INVALID_ARG;
-    p.part_o = static_cast<float*>(a->workspace);
-    p.part_lse = p.part_o + rows * p.D;
-  }
+  if (sp.bytes && (!a->workspace || !swa::aligned16(a->workspace) || a->workspace_bytes < sp.bytes))
+    return SWA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
+  if (sp.token) {
+    e = swa::launch_cache_token(p, sp.t, a->workspace, s);
+    return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+  }
+  if (p.nsplit > 1) {
+    p.part_o = static_cast<float*>(a->workspace);
+    p.part_lse = p.part_o + (size_t)p.nsplit * p.T * p.Hq * p.D;
+  }
   if (c->dtype == SWA_FP32)
     e = p.D == 64 ? swa::launch_core<float, 64>(p, sp.row_tiles, s) : swa::launch_core<float, 128>(p, sp.row_tiles, s);
   else

@@ -24,8 +24,9 @@ struct CacheAttendParams {
   const int32_t* seq_lens;          // [B]
   const int32_t* cu_tokens;         // [B + 1] or null
   int* err;
-  float* part_o;                    // [nsplit, T, Hq, D] unnormalised nowhere: each split's own softmax
-  float* part_lse;                  // [nsplit, T, Hq]
+  float* part_o;                    // partial results, each the softmax over its own keys
+  float* part_lse;
+  void* prefix;                     // few-token kernel: [B + 1] int64 first steps of the sequences
   long long q_token, q_head;        // strides of q, elements
   int B, T, Hq, Hkv, G, D;
   int num_pages, page_size, max_pages;
@@ -34,5 +35,16 @@ struct CacheAttendParams {
   int nsplit;                       // parts of a sequence's keys
   float scale, softcap;
 };
+
+// The few-token kernel (bf16, new tokens of a sequence x heads of a group <= kTokenRows):
+// how its warps are laid out, from sizes only.
+constexpr int kTokenRows = 32;
+struct TokenSplit {
+  int warps, blocks;                // warps of a block, blocks
+  int row_pad;                      // rows of a partial result
+  size_t bytes;                     // workspace
+};
+TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach);
+cudaError_t launch_cache_token(CacheAttendParams p, const TokenSplit& t, void* workspace, cudaStream_t s);
 
 }  // namespace swa

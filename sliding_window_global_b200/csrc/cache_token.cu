@@ -1,0 +1,523 @@
+// cache_token.cu -- attention over a paged cache when a sequence brings few new tokens
+// (bf16; new tokens x heads of a group <= 32 rows): decoding, and checking guessed tokens.
+//
+// The bound is the read of K and V once.  A KV head of a sequence is one unit: its rows
+// (new tokens x query heads of the group) fill one or two 16-row fragments, so that one
+// pass over the keys serves the whole group.  All units' keys, cut into steps of 16 (D =
+// 128) or 32 (D = 64) keys = 8 KB of K and V, form one list; every warp of the grid takes
+// an equal, contiguous run of it, whatever the lengths (the host does not know them).  A
+// warp works alone: it fetches its steps with cp.async into its own ring of three, and
+// keeps scores, running maximum, sum and output in registers (mma.sync m16n8k16: with 16
+// rows the tensor work is an eighth of the time that the bytes take, so that the
+// 128-row tcgen05 products would only compute padding).  A unit that lies in one warp's run
+// is stored directly; one that is split leaves a partial result a warp, which the merge
+// kernel joins in the order of the keys.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "cache_device.cuh"
+#include "ptx.cuh"
+
+namespace swa {
+namespace {
+
+constexpr int kStages = 3;
+constexpr int kMaxWarps = 8;               // warps of a block
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct Step {
+  static constexpr int kKeys = 2048 / D;               // 16 or 32
+  static constexpr int kGroups = kKeys / 16;           // 16-key groups: each lies in one page
+  static constexpr int kHalf = kKeys * D * 2;          // bytes of K (or V) of a step
+  static constexpr int kBytes = 2 * kHalf;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The steps of a sequence (the same for each of its KV heads): keys [lo, hi) of interest,
+// steps from the step-aligned start on.  A sequence with new tokens has one at least, so
+// that rows without a key are written too.
+struct TokenUnit {
+  CacheSeq s;
+  int lo, hi, base, steps;
+};
+
+template <int D>
+__device__ __forceinline__ TokenUnit token_unit(const CacheAttendParams& p, int b) {
+  TokenUnit u;
+  u.s = cache_seq(p, b);
+  u.lo = u.hi = u.base = u.steps = 0;
+  if (u.s.count > 0) {
+    u.lo = key_begin(p, u.s, 0);
+    u.hi = max(u.lo, key_end(u.s, u.s.count - 1));
+    u.base = u.lo / Step<D>::kKeys * Step<D>::kKeys;
+    u.steps = max(1, (u.hi - u.base + Step<D>::kKeys - 1) / Step<D>::kKeys);
+  }
+  return u;
+}
+
+// Sum of the steps of all units, by one warp; each lane calls each(b, the first step of
+// sequence b's units, their number, whether something of b's bounds does not hold).
+template <int D, typename F>
+__device__ __forceinline__ long long scan_steps(const CacheAttendParams& p, int lane, F each) {
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    long long mine = 0;
+    bool bad = false;
+    if (b < p.B) {
+      const TokenUnit u = token_unit<D>(p, b);
+      mine = (long long)u.steps * p.Hkv;
+      bad = u.s.bad;
+    }
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    each(b, before + sum - mine, mine, bad);
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return before;
+}
+
+// Run of warp w of W over n steps: [run_begin(w), run_begin(w + 1)).
+__device__ __forceinline__ long long run_begin(long long n, int w, int W) { return n * w / W; }
+
+template <int D, int MT, bool CAP>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __grid_constant__ CacheAttendParams p) {
+  using S = Step<D>;
+  constexpr int NG = S::kGroups;
+  constexpr int CH = D / 8;                            // 16-byte chunks of a row
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31;
+  const int w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), W = gridDim.x * (blockDim.x >> 5);
+  const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * kStages * S::kBytes;
+  grid_launch_dependents();
+
+  // ---- this warp's run, and the sequence, head and step it starts at
+  long long* prefix = reinterpret_cast<long long*>(p.prefix);
+  const long long n = scan_steps<D>(p, lane, [&](int b, long long first, long long, bool bad) {
+    if (w != 0 || b >= p.B) return;
+    prefix[b] = first;
+    if (bad) atomicOr(p.err, kDevErrCheck);
+  });
+  if (w == 0 && lane == 0) prefix[p.B] = n;
+  const long long begin = run_begin(n, w, W);
+  const int total = (int)(run_begin(n, w + 1, W) - begin);
+  if (total == 0) return;
+  int b = 0, hk = 0, j = 0;
+  {
+    int fb = 0;
+    long long ff = 0;
+    scan_steps<D>(p, lane, [&](int bb, long long first, long long mine, bool) {
+      const unsigned hit = __ballot_sync(0xffffffffu, bb < p.B && first <= begin && begin < first + mine);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        fb = __shfl_sync(0xffffffffu, bb, src);
+        ff = __shfl_sync(0xffffffffu, first, src);
+      }
+    });
+    const int steps = token_unit<D>(p, fb).steps;
+    b = fb;
+    hk = (int)((begin - ff) / steps);
+    j = (int)((begin - ff) % steps);
+  }
+
+  // ---- fetching side: its own place in the list, kStages - 1 steps ahead
+  TokenUnit fu = token_unit<D>(p, b);
+  int fb = b, fhk = hk, fj = j;
+  int fpage[NG];
+  unsigned history = 0;                    // per group of a fetched step: its page exists (newest lowest)
+  auto look_up = [&]() {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int key = fu.base + fj * S::kKeys + 16 * g;
+      fpage[g] = key < fu.hi ? __ldg(p.block_table + (long long)fb * p.max_pages + key / p.page_size) : 0;
+    }
+  };
+  look_up();
+  int fetched = 0;
+  auto fetch = [&]() {
+    if (fetched < total) {
+      const uint32_t dst = ring + fetched % kStages * S::kBytes;
+      const int key0 = fu.base + fj * S::kKeys;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int key = key0 + 16 * g;
+        const bool ok = fpage[g] >= 0 && fpage[g] < p.num_pages;
+        if (!ok && lane == 0) atomicOr(p.err, kDevErrCheck);
+        history = history << 1 | (ok ? 1u : 0u);
+        const long long off = (((long long)(ok ? fpage[g] : 0) * p.Hkv + fhk) * p.page_size + key % p.page_size) * D;
+        const __nv_bfloat16* ks = static_cast<const __nv_bfloat16*>(p.k_pages) + off;
+        const __nv_bfloat16* vs = static_cast<const __nv_bfloat16*>(p.v_pages) + off;
+#pragma unroll
+        for (int i = 0; i < 16 * CH / 32; ++i) {
+          const int c = lane + 32 * i, row = c / CH, col = c % CH;
+          const bool on = ok && key + row >= fu.lo && key + row < fu.hi;   // else zeros: V times p = 0 must stay 0
+          const uint32_t at = dst + ((16 * g + row) * CH + (col ^ (row & 7))) * 16;
+          cp_async16(at, ks + c * 8, on);
+          cp_async16(at + S::kHalf, vs + c * 8, on);
+        }
+      }
+      ++fetched;
+      if (++fj == fu.steps) {
+        fj = 0;
+        if (++fhk == p.Hkv) {
+          fhk = 0;
+          do {
+            ++fb;
+          } while (fb < p.B && (fu = token_unit<D>(p, fb)).steps == 0);
+        }
+      }
+      if (fetched < total) look_up();
+    } else {
+      history <<= NG;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) fetch();
+
+  // ---- computing side
+  const float sl2 = p.scale * kLog2e;
+  const float cap_l2 = p.softcap * kLog2e;             // CAP: cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+  const float cap_in = CAP ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
+  int done = 0;
+  while (done < total) {
+    const TokenUnit u = token_unit<D>(p, b);
+    const int rows = u.s.count * p.G;
+    uint32_t qf[MT][D / 16][4];
+    int klo[MT][2], khi[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const __nv_bfloat16* src[2];
+      bool live[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = mt * 16 + (lane >> 2) + 8 * x;
+        live[x] = r < rows;
+        const int tok = live[x] ? r / p.G : 0, h = hk * p.G + (live[x] ? r % p.G : 0);
+        klo[mt][x] = live[x] ? key_begin(p, u.s, tok) : 0;
+        khi[mt][x] = live[x] ? key_end(u.s, tok) : 0;
+        src[x] = static_cast<const __nv_bfloat16*>(p.q) + (long long)(u.s.from + tok) * p.q_token + h * p.q_head +
+                 2 * (lane & 3);
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          qf[mt][kk][x] = live[x & 1] ? *reinterpret_cast<const uint32_t*>(src[x & 1] + 16 * kk + 8 * (x >> 1)) : 0u;
+      }
+    }
+    // keys that every row of the unit sees need no mask
+    const int full_lo = key_begin(p, u.s, u.s.count - 1);
+    const int full_hi = key_end(u.s, 0);
+    float o[MT][D / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[mt][e][c] = 0.f;
+    }
+    const bool from_start = j == 0;
+    while (true) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      fetch();                             // into the slot of the step before, which every lane has read
+      const uint32_t at = ring + done % kStages * S::kBytes;
+      const unsigned pages = history >> ((kStages - 1) * NG) & ((1u << NG) - 1);
+      const int key0 = u.base + j * S::kKeys;
+
+      float s[MT][2 * NG][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int t = 0; t < 2 * NG; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[mt][t][c] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          uint32_t kf[4];
+          const int row = (lane & 7) + ((lane >> 4) << 3), col = 2 * kk + ((lane >> 3) & 1);
+          ldmatrix4(kf, at + ((16 * g + row) * CH + (col ^ (row & 7))) * 16);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma_bf16(s[mt][2 * g], qf[mt][kk], kf[0], kf[1]);
+            mma_bf16(s[mt][2 * g + 1], qf[mt][kk], kf[2], kf[3]);
+          }
+        }
+      }
+      const bool masked = key0 < full_lo || key0 + S::kKeys > full_hi || pages != (1u << NG) - 1;
+      uint32_t pf[MT][NG][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float mx[2] = {m[mt][0], m[mt][1]};
+#pragma unroll
+        for (int t = 0; t < 2 * NG; ++t) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float x = s[mt][t][c];
+            if (CAP) x = cap_l2 - 2.f * cap_l2 * __frcp_rn(1.f + ex2_approx(x * cap_in));
+            else x *= sl2;
+            if (masked) {
+              const int key = key0 + 8 * t + 2 * (lane & 3) + (c & 1);
+              const bool see = key >= klo[mt][c >> 1] && key < khi[mt][c >> 1] && (pages >> (NG - 1 - t / 2) & 1);
+              x = see ? x : -INFINITY;
+            }
+            s[mt][t][c] = x;
+            mx[c >> 1] = fmaxf(mx[c >> 1], x);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+          mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] > m[mt][0] || mx[1] > m[mt][1])) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float alpha = m[mt][x] == -INFINITY ? 0.f : ex2_approx(m[mt][x] - mx[x]);
+            m[mt][x] = mx[x];
+            l[mt][x] *= alpha;
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e) {
+              o[mt][e][2 * x] *= alpha;
+              o[mt][e][2 * x + 1] *= alpha;
+            }
+          }
+        }
+        const float ref[2] = {m[mt][0] == -INFINITY ? 0.f : m[mt][0], m[mt][1] == -INFINITY ? 0.f : m[mt][1]};
+#pragma unroll
+        for (int t = 0; t < 2 * NG; ++t) {
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            e[c] = ex2_approx(s[mt][t][c] - ref[c >> 1]);
+            l[mt][c >> 1] += e[c];
+          }
+          // p in bf16: the type of the tensor product that follows; the sum keeps 32 bits
+          pf[mt][t / 2][2 * (t & 1)] = pack_bf16x2(e[0], e[1]);
+          pf[mt][t / 2][2 * (t & 1) + 1] = pack_bf16x2(e[2], e[3]);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          uint32_t vf[4];
+          const int row = (lane & 7) + (((lane >> 3) & 1) << 3), col = 2 * e + (lane >> 4);
+          ldmatrix4_trans(vf, at + S::kHalf + ((16 * g + row) * CH + (col ^ (row & 7))) * 16);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma_bf16(o[mt][2 * e], pf[mt][g], vf[0], vf[1]);
+            mma_bf16(o[mt][2 * e + 1], pf[mt][g], vf[2], vf[3]);
+          }
+        }
+      }
+      ++done;
+      ++j;
+      if (j == u.steps || done == total) break;
+    }
+
+    // ---- the unit (or this run's part of it) is done
+    const bool whole = from_start && j == u.steps;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float sum = l[mt][x];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = mt * 16 + (lane >> 2) + 8 * x;
+        if (r >= rows) continue;
+        const bool has = m[mt][x] != -INFINITY;
+        const float inv = has ? 1.f / sum : 0.f;
+        const float lse = has ? (m[mt][x] + log2f(sum)) * kLn2 : -INFINITY;
+        if (whole) {
+          const long long row = (long long)(u.s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
+          uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + row * D + 2 * (lane & 3));
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e) out[4 * e] = pack_bf16x2(o[mt][e][2 * x] * inv, o[mt][e][2 * x + 1] * inv);
+          if (p.lse && (lane & 3) == 0) p.lse[row] = lse;
+        } else {
+          const long long row = (2LL * w + (from_start ? 1 : 0)) * (16 * MT) + r;
+          float2* part = reinterpret_cast<float2*>(p.part_o + row * D + 2 * (lane & 3));
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e) part[4 * e] = make_float2(o[mt][e][2 * x] * inv, o[mt][e][2 * x + 1] * inv);
+          if ((lane & 3) == 0) p.part_lse[row] = lse;
+        }
+      }
+    }
+    if (j == u.steps) {
+      j = 0;
+      if (++hk == p.Hkv) {
+        hk = 0;
+        if (done < total) {
+          do {
+            ++b;
+          } while (token_unit<D>(p, b).steps == 0);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the parts of every row whose unit was split: one block a row, its warps take the
+// parts in turn and are added up in order, so the same call gives the same bits.
+template <int D>
+__global__ void __launch_bounds__(128) cache_token_merge_kernel(const __grid_constant__ CacheAttendParams p, int W,
+                                                                 int row_pad) {
+  constexpr int E = D / 32;
+  __shared__ float sO[4][D], sM[4], sL[4];
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  const int max_rows = p.max_tokens * p.G;
+  const int r = blockIdx.x % max_rows;
+  const int hk = blockIdx.x / max_rows % p.Hkv;
+  const int b = blockIdx.x / max_rows / p.Hkv;
+  const long long* prefix = reinterpret_cast<const long long*>(p.prefix);
+  const long long first = prefix[b], steps = (prefix[b + 1] - first) / p.Hkv, n = prefix[p.B];
+  if (steps == 0) return;
+  const CacheSeq s = cache_seq(p, b);
+  if (r >= s.count * p.G) return;
+  const long long u0 = first + hk * steps, u1 = u0 + steps;
+  // the runs that hold the unit's first and last step
+  auto run_of = [&](long long step) {
+    int w = (int)(step * W / n);
+    while (w + 1 < W && run_begin(n, w + 1, W) <= step) ++w;
+    while (run_begin(n, w, W) > step) --w;
+    return w;
+  };
+  const int w0 = run_of(u0), w1 = run_of(u1 - 1);
+  if (w0 == w1) return;                    // stored whole
+  float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int w = w0 + wp; w <= w1; w += 4) {
+    const long long at = run_begin(n, w, W);
+    if (at == run_begin(n, w + 1, W)) continue;          // an empty run (fewer steps than warps)
+    const long long row = (2LL * w + (at <= u0 ? 1 : 0)) * row_pad + r;
+    const float lse = p.part_lse[row];
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = p.part_o[row * D + lane + 32 * e];
+    if (lse == -INFINITY) continue;        // no key in this part (a NaN goes on)
+    const float mx = fmaxf(m, lse);
+    const float keep = m == -INFINITY ? 0.f : ex2_approx((m - mx) * kLog2e), f = ex2_approx((lse - mx) * kLog2e);
+    m = mx;
+    l = l * keep + f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + f * x[e];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sO[wp][lane + 32 * e] = o[e];
+  if (lane == 0) {
+    sM[wp] = m;
+    sL[wp] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float top = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = fmaxf(top, sM[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sL[i] == 0.f) continue;
+    const float f = ex2_approx((sM[i] - top) * kLog2e);
+    sum += f * sL[i];
+    acc += f * sO[i][threadIdx.x];
+  }
+  const bool has = sum != 0.f;
+  const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
+  static_cast<__nv_bfloat16*>(p.out)[row * D + threadIdx.x] = __float2bfloat16_rn(has ? acc / sum : 0.f);
+  if (p.lse && threadIdx.x == 0) p.lse[row] = has ? top + log2f(sum) * kLn2 : -INFINITY;
+}
+
+template <int D, int MT, bool CAP>
+cudaError_t launch_token(const CacheAttendParams& p, const TokenSplit& t, cudaStream_t s) {
+  auto kern = cache_token_kernel<D, MT, CAP>;
+  const int smem = t.warps * kStages * Step<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kMaxWarps * kStages * Step<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<t.blocks, t.warps * 32, smem, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.max_tokens * p.G));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_token_merge_kernel<D>, p, t.blocks * t.warps, 16 * MT);
+}
+
+}  // namespace
+
+TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach) {
+  TokenSplit t;
+  t.row_pad = rows <= 16 ? 16 : 32;
+  const int keys = 2048 / D;
+  const long long steps = (long long)B * Hkv * ((reach + keys - 1) / keys + 1);
+  // Two steps a warp at least; one block an SM, of as few warps as that allows.
+  const long long want = std::min<long long>((steps + 1) / 2, 148 * kMaxWarps);
+  t.warps = 1;
+  while (t.warps < kMaxWarps && 148 * t.warps < want) t.warps *= 2;
+  t.blocks = (int)((want + t.warps - 1) / t.warps);
+  t.bytes = (((size_t)B + 1) * 8 + 15) / 16 * 16 + (size_t)2 * t.blocks * t.warps * t.row_pad * (D + 1) * 4;
+  return t;
+}
+
+cudaError_t launch_cache_token(CacheAttendParams p, const TokenSplit& t, void* workspace, cudaStream_t s) {
+  p.prefix = workspace;
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + (((size_t)p.B + 1) * 8 + 15) / 16 * 16);
+  p.part_lse = p.part_o + (size_t)2 * t.blocks * t.warps * t.row_pad * p.D;
+  const bool cap = p.softcap > 0.f;
+  if (p.D == 64) {
+    if (t.row_pad == 16) return cap ? launch_token<64, 1, true>(p, t, s) : launch_token<64, 1, false>(p, t, s);
+    return cap ? launch_token<64, 2, true>(p, t, s) : launch_token<64, 2, false>(p, t, s);
+  }
+  if (t.row_pad == 16) return cap ? launch_token<128, 1, true>(p, t, s) : launch_token<128, 1, false>(p, t, s);
+  return cap ? launch_token<128, 2, true>(p, t, s) : launch_token<128, 2, false>(p, t, s);
+}
+
+}  // namespace swa

@@ -381,14 +381,22 @@ def test_broken_bounds_stay_in_bounds(new):
 
     st, good, good_lse = run()
     assert st == 0
+    ref = reference(s, q, None, 0.0, 0.0, 4)
+
+    def first_holds(out, lse):
+        # Not bit for bit: where the keys of a sequence are parted depends on all lengths,
+        # and parts are joined in fp32.  Every parting meets the definition's own bound.
+        check_attention(out[:c], lse[:c], [x[:c] for x in ref], BF16)
+        return True
+
     i32 = dict(dtype=torch.int32, device="cuda")
     st, out, lse = run(lens=torch.tensor([200, -3], **i32))
-    assert st == DEVICE_CHECK and torch.equal(out[:c], good[:c])
+    assert st == DEVICE_CHECK and first_holds(out, lse)
     assert not out[c:].any() and bool(torch.isneginf(lse[c:]).all())
     st, out, lse = run(cu=torch.tensor([0, c, T + 5], **i32))
-    assert st == DEVICE_CHECK and torch.equal(out[:c], good[:c]) and bool((out[c:] == 7.0).all())
+    assert st == DEVICE_CHECK and first_holds(out, lse) and bool((out[c:] == 7.0).all())
     st, out, lse = run(cu=torch.tensor([0, c, c - 1], **i32))
-    assert st == DEVICE_CHECK and torch.equal(out[:c], good[:c]) and bool((out[c:] == 7.0).all())
+    assert st == DEVICE_CHECK and first_holds(out, lse) and bool((out[c:] == 7.0).all())
     st, out, lse = run(max_tokens=c - 1)                   # the last token of each is left out
     assert st == DEVICE_CHECK and bool((out[c - 1] == 7.0).all()) and bool((out[T - 1] == 7.0).all())
     assert bool(((out[0].float() - good[0].float()).abs() <= 2.0 ** -6 * (1 + good[0].float().abs())).all())
