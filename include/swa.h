@@ -501,7 +501,7 @@ swa_status swa_cache_append(const swa_cache* cache, const swa_cache_batch* batch
  * turn NaN. */
 typedef struct {
   int num_q_heads;             /* a multiple of the cache's num_kv_heads, <= 128 */
-  const void* q;               /* device [T, Hq, D], strides (token, head) */
+  const void* q;               /* device [T, Hq, D], strides (token, head), positive */
   int64_t q_stride[2];
   int max_tokens;              /* no sequence has more new tokens (ignored without cu_tokens) */
   int max_len;                 /* no seq_lens[b] is larger; 0: max_pages * page_size */

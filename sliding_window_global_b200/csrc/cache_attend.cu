@@ -1,10 +1,10 @@
-// cache_attend.cu -- attention over a paged cache: the entry points, the CUDA-core
-// kernel, and the merge of split sequences.  The definition stands in include/swa.h.
+// cache_attend.cu -- attention over a paged cache: the entry points, and the fp32 kernel
+// with the merge of its split sequences.  bf16 runs in cache_token.cu (few new tokens a
+// sequence) and cache_chunk.cu (many).  The definition stands in include/swa.h.
 //
 // A row is one (new token, query head) pair; the rows of a KV head's query heads are
 // packed token by token (row r = token * G + head in the group), so that a key tile is
 // read once for the whole group.
-#include <cuda_bf16.h>
 #include <math.h>
 
 #include <algorithm>
@@ -27,7 +27,7 @@ constexpr int core_smem_bytes() {
 // 64 rows x 64 keys a step in fp32 on the FMA pipe, each thread 4 x 4 scores and
 // 4 x D/16 outputs; K and V take turns in one shared buffer so that two blocks fit on
 // an SM and one computes while the other loads.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_constant__ CacheAttendParams p,
                                                                   int row_tiles) {
   constexpr int LD = D + 4, LP = kKeys + 4;
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
     float x[8];
     if (r0 + r < rows) {
       const int tok = (r0 + r) / p.G, h = hk * p.G + (r0 + r) % p.G;
-      unpack(load_chunk(static_cast<const T*>(p.q) + (long long)(s.from + tok) * p.q_token + h * p.q_head + c), x);
+      unpack(load_chunk(static_cast<const float*>(p.q) + (long long)(s.from + tok) * p.q_token + h * p.q_head + c), x);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = 0.f;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
           const int page = __ldg(p.block_table + (long long)b * p.max_pages + pos / p.page_size);
           ok = page >= 0 && page < p.num_pages;
           if (ok)
-            unpack(load_chunk(static_cast<const T*>(pages) +
+            unpack(load_chunk(static_cast<const float*>(pages) +
                               (((long long)page * p.Hkv + hk) * p.page_size + pos % p.page_size) * D + c), x);
           else if (keys && c == 0) atomicOr(p.err, kDevErrCheck);
         }
@@ -200,11 +200,11 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
             make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
       if (tx == 0) p.part_lse[pr] = lse;
     } else {
-      T* out = static_cast<T*>(p.out) + row * D;
+      float* out = static_cast<float*>(p.out) + row * D;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[tx * 4 + 64 * c + e] = static_cast<T>(o[i][4 * c + e] * inv);
+        for (int e = 0; e < 4; ++e) out[tx * 4 + 64 * c + e] = o[i][4 * c + e] * inv;
       if (p.lse && tx == 0) p.lse[row] = lse;
     }
   }
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
 
 // out = sum_s exp(lse_s - lse) out_s over the splits in order, lse = log sum_s exp(lse_s):
 // one warp a row.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant__ CacheAttendParams p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
@@ -239,16 +239,16 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
   }
   const bool has = sum != 0.f;
   const float inv = has ? 1.f / sum : 0.f;
-  T* out = static_cast<T*>(p.out) + row * D + lane * E;
+  float* out = static_cast<float*>(p.out) + row * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = static_cast<T>(acc[e] * inv);
+  for (int e = 0; e < E; ++e) out[e] = acc[e] * inv;
   if (p.lse && lane == 0) p.lse[row] = has ? top + logf(sum) : -INFINITY;
 }
 
 // ------------------------------------------------------------------ launches
-template <typename T, int D>
+template <int D>
 cudaError_t launch_core(const CacheAttendParams& p, int row_tiles, cudaStream_t s) {
-  auto kern = cache_core_kernel<T, D>;
+  auto kern = cache_core_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, core_smem_bytes<D>());
   if (e != cudaSuccess) return e;
   kern<<<dim3((unsigned)((long long)p.B * row_tiles * p.nsplit), p.Hkv), kCoreThreads, core_smem_bytes<D>(), s>>>(
@@ -256,19 +256,19 @@ cudaError_t launch_core(const CacheAttendParams& p, int row_tiles, cudaStream_t 
   return cudaGetLastError();
 }
 
-template <typename T>
 cudaError_t launch_merge(const CacheAttendParams& p, cudaStream_t s) {
   const long long rows = (long long)p.B * p.max_tokens * p.Hq;
   const unsigned blocks = (unsigned)((rows + 3) / 4);
-  if (p.D == 64) cache_merge_kernel<T, 64><<<blocks, 128, 0, s>>>(p);
-  else cache_merge_kernel<T, 128><<<blocks, 128, 0, s>>>(p);
+  if (p.D == 64) cache_merge_kernel<64><<<blocks, 128, 0, s>>>(p);
+  else cache_merge_kernel<128><<<blocks, 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 // How a call is cut up, from sizes only: which kernel, and its parts.
 struct AttendSplit {
-  bool token;                              // the few-token kernel
-  TokenSplit t;
+  enum { kToken, kChunk, kCore } kernel;
+  TokenSplit token;
+  ChunkSplit chunk;
   int row_tiles, nsplit;                   // CUDA-core kernel: tiles of rows, parts of the keys
   size_t bytes;                            // workspace
 };
@@ -279,12 +279,20 @@ AttendSplit attend_split(const swa_cache& c, const swa_cache_batch& b, const swa
   const int G = a.num_q_heads / c.num_kv_heads;
   // keys a sequence's new tokens can reach
   const long long reach = a.window < 0 ? max_len : std::min<long long>(max_len, (long long)a.window + max_tokens);
-  if (c.dtype == SWA_BF16 && (long long)max_tokens * G <= kTokenRows) {
-    r.token = true;
-    r.t = token_split(b.batch, c.num_kv_heads, c.head_dim, max_tokens * G, reach);
-    r.bytes = r.t.bytes;
+  // fp32 stays on the FMA pipe: the tensor core's products would keep 11 bits of it
+  if (c.dtype == SWA_BF16) {
+    if ((long long)max_tokens * G <= kTokenRows) {
+      r.kernel = AttendSplit::kToken;
+      r.token = token_split(b.batch, c.num_kv_heads, c.head_dim, max_tokens * G, reach);
+      r.bytes = r.token.bytes;
+    } else {
+      r.kernel = AttendSplit::kChunk;
+      r.chunk = chunk_split(b.batch, b.num_tokens, c.num_kv_heads, G, c.head_dim, c.page_size, max_len, a.window);
+      r.bytes = r.chunk.bytes;
+    }
     return r;
   }
+  r.kernel = AttendSplit::kCore;
   r.row_tiles = (int)(((long long)max_tokens * G + kRows - 1) / kRows);
   // parts of at least 256 keys, two blocks an SM
   const long long blocks = (long long)b.batch * r.row_tiles * c.num_kv_heads;
@@ -360,8 +368,8 @@ swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const 
   if (b->batch == 0 || b->num_tokens == 0 || p.max_tokens == 0) return SWA_OK;
   const int64_t unit = c->dtype == SWA_FP32 ? 4 : 8;
   if (!a->q || !a->out || !swa::aligned16(a->q) || !swa::aligned16(a->out) || !swa::aligned4(a->lse) ||
-      (b->num_tokens > 1 && (a->q_stride[0] < 0 || a->q_stride[0] % unit)) ||
-      (a->num_q_heads > 1 && (a->q_stride[1] < 0 || a->q_stride[1] % unit)))
+      (b->num_tokens > 1 && (a->q_stride[0] <= 0 || a->q_stride[0] % unit)) ||
+      (a->num_q_heads > 1 && (a->q_stride[1] <= 0 || a->q_stride[1] % unit)))
     return SWA_ERR_INVALID_ARG;
   const swa::AttendSplit sp = swa::attend_split(*c, *b, *a, p.max_tokens, p.max_len);
   p.k_pages = c->k_pages;
@@ -392,21 +400,20 @@ swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const 
     return SWA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (sp.token) {
-    e = swa::launch_cache_token(p, sp.t, a->workspace, s);
+  if (sp.kernel == swa::AttendSplit::kToken) {
+    e = swa::launch_cache_token(p, sp.token, a->workspace, s);
+    return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+  }
+  if (sp.kernel == swa::AttendSplit::kChunk) {
+    e = swa::launch_cache_chunk(p, sp.chunk, a->workspace, s);
     return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
   }
   if (p.nsplit > 1) {
     p.part_o = static_cast<float*>(a->workspace);
     p.part_lse = p.part_o + (size_t)p.nsplit * p.T * p.Hq * p.D;
   }
-  if (c->dtype == SWA_FP32)
-    e = p.D == 64 ? swa::launch_core<float, 64>(p, sp.row_tiles, s) : swa::launch_core<float, 128>(p, sp.row_tiles, s);
-  else
-    e = p.D == 64 ? swa::launch_core<__nv_bfloat16, 64>(p, sp.row_tiles, s)
-                  : swa::launch_core<__nv_bfloat16, 128>(p, sp.row_tiles, s);
-  if (e == cudaSuccess && p.nsplit > 1)
-    e = c->dtype == SWA_FP32 ? swa::launch_merge<float>(p, s) : swa::launch_merge<__nv_bfloat16>(p, s);
+  e = p.D == 64 ? swa::launch_core<64>(p, sp.row_tiles, s) : swa::launch_core<128>(p, sp.row_tiles, s);
+  if (e == cudaSuccess && p.nsplit > 1) e = swa::launch_merge(p, s);
   return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 

@@ -1,0 +1,820 @@
+// cache_chunk.cu -- attention over a paged cache when sequences bring many new tokens
+// (bf16): prompts and their chunks.
+//
+// The bound is the tensor core. A query tile holds floor(128 / G) tokens with the G query
+// heads of one KV head, so its 128 TMEM lanes share every key; a unit is two such tiles (A
+// and B, consecutive tokens) of one KV head, which share every key tile they both see. Key
+// tiles of 128 positions come from the pages by TMA, in boxes that never cross a page
+// (16 to 128 keys); positions that do not exist are asked for outside the tensor map,
+// which fills them with zeros. As in the band kernel (band_tc.cu): S = Q K^T by
+// tcgen05.mma into TMEM, one thread per row for the softmax, P written over S, O += P V with
+// P read from TMEM, a lazy rescale of O.
+//
+// Sequences' lengths are known on the device only, so a small kernel first lists the token
+// tiles and cuts the list of all units' key tiles into one equal run for each block. A unit
+// that a cut goes through leaves a partial result in each of its runs, joined afterwards in
+// the order of the keys; short units are never cut.
+//
+// Warp roles: 0-3 softmax of tile A, 4-7 of tile B, 8 loads, 9 MMAs, 10 zeroes the values at
+// positions outside the unit's keys (P is 0 there, but 0 times a NaN would not be).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "cache_device.cuh"
+#include "ptx.cuh"
+#include "softmax_math.cuh"
+#include "swa_host.h"
+
+namespace swa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 200, kRegsControl = 104;     // 256 * 200 + 128 * 104 = 384 * 168
+constexpr int kStages = 2;
+constexpr uint32_t kSub = 128 * 128;                      // 128 rows of 128 bytes, swizzled
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;                 // log2 units
+constexpr int kShortUnit = 16;                            // units of fewer key tiles are not cut
+constexpr int kMinPiece = 4;                              // nor is a unit cut this close to its ends
+constexpr int kUnitRows = 2 * kTile;
+
+// One token tile pair of a sequence.
+struct ChunkEntry {
+  long long first;                 // first step (key tile) of its units: KV head 0, 1, ...
+  int b;
+  int row0;                        // row of the first token in the packed tensors
+  int tokens;
+  int pos0;                        // position of the first token
+  int limit;                       // keys exist below this
+  int base, tiles;                 // first key of key tile 0, key tiles
+  int pad;
+};
+
+// Where a run starts; the entry behind the last run is the end of the list.
+struct ChunkRun {
+  long long step;
+  int entry, hk, j;
+  int inside;                      // the cut goes through a unit
+};
+
+struct ChunkPlan {
+  int entries;
+  int pad;
+  long long steps;
+};
+
+struct ChunkParams {
+  CUtensorMap mq, mk, mv;
+  CacheAttendParams a;
+  ChunkPlan* plan;
+  int* entry_first;                // [B + 1] first entry of each sequence
+  ChunkEntry* entries;
+  ChunkRun* runs;                  // [runs + 1]
+  float* part_o;                   // [runs, 2, 256, D]
+  float* part_lse;                 // [runs, 2, 256]
+  int num_runs, tile_tokens, box, max_entries;
+  float scale_log2;
+};
+
+// ------------------------------------------------------------------ the list of work
+constexpr int kPlanThreads = 512;
+
+// Inclusive sums over the block's threads; every thread calls it.
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += up;
+  }
+  __syncthreads();                                       // the sums of the call before are read
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  long long before = 0, all = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += warp_sums[w];
+    all += warp_sums[w];
+  }
+  total = all;
+  return x + before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ long long warp_sums[kPlanThreads / 32];
+  const CacheAttendParams& a = p.a;
+  const int pair = 2 * p.tile_tokens;
+  grid_launch_dependents();
+  // token tile pairs of each sequence
+  long long total, before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    long long n = 0;
+    if (b < a.B) {
+      const CacheSeq s = cache_seq(a, b);
+      if (s.bad) atomicOr(a.err, kDevErrCheck);
+      n = (s.count + pair - 1) / pair;
+    }
+    const long long upto = block_scan(n, warp_sums, total);
+    if (b < a.B) p.entry_first[b] = (int)min(before + upto - n, (long long)p.max_entries);
+    before += total;
+  }
+  const int entries = (int)min(before, (long long)p.max_entries);   // overlapping cu_tokens may name more rows than T
+  if (threadIdx.x == 0) p.entry_first[a.B] = entries;
+  __syncthreads();
+  // their keys, and the first step of each
+  long long steps = 0;
+  for (int e0 = 0; e0 < entries; e0 += kPlanThreads) {
+    const int e = e0 + threadIdx.x;
+    ChunkEntry r = {};
+    long long n = 0;
+    if (e < entries) {
+      int lo = 0, hi = a.B - 1;                          // the last sequence that starts at or before e
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.entry_first[mid] <= e) lo = mid;
+        else hi = mid - 1;
+      }
+      const CacheSeq s = cache_seq(a, lo);
+      const int t0 = (e - p.entry_first[lo]) * pair;
+      r.b = lo;
+      r.row0 = s.from + t0;
+      r.tokens = min(pair, s.count - t0);
+      r.pos0 = s.pos0 + t0;
+      r.limit = s.limit;
+      const int k0 = key_begin(a, s, t0), k1 = key_end(s, t0 + r.tokens - 1);
+      r.base = k0 / p.box * p.box;
+      r.tiles = k1 > k0 ? (k1 - r.base + kTile - 1) / kTile : 1;
+      n = (long long)r.tiles * a.Hkv;
+    }
+    const long long upto = block_scan(n, warp_sums, total);
+    r.first = steps + upto - n;
+    if (e < entries) p.entries[e] = r;
+    steps += total;
+  }
+  if (threadIdx.x == 0) {
+    p.plan->entries = entries;
+    p.plan->steps = steps;
+  }
+  __syncthreads();
+  // equal runs, their cuts moved to a unit's edge where the unit is short or the edge near
+  for (int c = threadIdx.x; c <= p.num_runs; c += kPlanThreads) {
+    const long long x = steps * c / p.num_runs;
+    ChunkRun r = {x, entries, 0, 0, 0};
+    if (x < steps) {
+      int lo = 0, hi = entries - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.entries[mid].first <= x) lo = mid;
+        else hi = mid - 1;
+      }
+      const ChunkEntry& en = p.entries[lo];
+      r.entry = lo;
+      r.hk = (int)((x - en.first) / en.tiles);
+      r.j = (int)((x - en.first) % en.tiles);
+      const bool to_start = en.tiles <= kShortUnit ? 2 * r.j < en.tiles : r.j < kMinPiece;
+      const bool to_end = en.tiles <= kShortUnit ? !to_start : en.tiles - r.j < kMinPiece;
+      if (to_start) {
+        r.step -= r.j;
+        r.j = 0;
+      } else if (to_end) {
+        r.step += en.tiles - r.j;
+        r.j = 0;
+        if (++r.hk == a.Hkv) {
+          r.hk = 0;
+          ++r.entry;
+        }
+      }
+      r.inside = r.j > 0;
+    }
+    p.runs[c] = r;
+  }
+}
+
+// ------------------------------------------------------------------ a run's pieces
+// Key tiles [j0, j1) of one unit.
+struct Piece {
+  ChunkEntry en;
+  int hk, j0, j1;
+};
+
+// One query tile of a piece: its rows and the key tiles [a, e) it uses.
+struct Half {
+  int tok0, tokens;                // first token in the entry, tokens
+  int lo, hi;                      // keys its rows see
+  int a, e;
+};
+
+__device__ __forceinline__ Half half_of(const ChunkParams& p, const Piece& pc, int x) {
+  Half h;
+  h.tok0 = x * p.tile_tokens;
+  h.tokens = min(max(pc.en.tokens - h.tok0, 0), p.tile_tokens);
+  const int pos = pc.en.pos0 + h.tok0;
+  h.lo = p.a.window < 0 ? 0 : (int)max(0LL, (long long)pos - p.a.window);
+  h.hi = min(pos + h.tokens, pc.en.limit);
+  // rows without a key still take part in one tile, so that they are written
+  int a = min(max(h.lo - pc.en.base, 0) / kTile, pc.en.tiles - 1);
+  int e = h.hi > h.lo ? min((h.hi - pc.en.base + kTile - 1) / kTile, pc.en.tiles) : a + 1;
+  h.a = max(a, pc.j0);
+  h.e = h.tokens > 0 ? max(h.a, min(e, pc.j1)) : h.a;
+  return h;
+}
+
+// The pieces of a block's run, in order; every warp role walks them alike.
+struct Walk {
+  long long left;
+  int entry, hk, j;
+  __device__ __forceinline__ Walk(const ChunkParams& p) {
+    const ChunkRun& r = p.runs[blockIdx.x];
+    left = p.runs[blockIdx.x + 1].step - r.step;
+    entry = r.entry;
+    hk = r.hk;
+    j = r.j;
+  }
+  __device__ __forceinline__ bool next(const ChunkParams& p, Piece& pc) {
+    if (left <= 0) return false;
+    pc.en = p.entries[entry];
+    pc.hk = hk;
+    pc.j0 = j;
+    pc.j1 = (int)min((long long)pc.en.tiles, j + left);
+    left -= pc.j1 - pc.j0;
+    j = 0;
+    if (++hk == p.a.Hkv) {
+      hk = 0;
+      ++entry;
+    }
+    return true;
+  }
+};
+
+template <int D>
+struct ChunkCfg {
+  static constexpr uint32_t kTileBytes = 128u * D * 2u;
+  static constexpr uint32_t kKOff = 2 * kTileBytes;
+  static constexpr uint32_t kVOff = kKOff + kStages * kTileBytes;
+  static constexpr uint32_t kBarOff = kVOff + kStages * kTileBytes;
+  static constexpr int kNumBars = 2 + 2 + 4 * kStages + 2 + 2 + 2 + 2;
+  static constexpr uint32_t kSmemBytes = kBarOff + kNumBars * 8 + 1024;
+  static constexpr uint32_t kTmemCols = 512;
+  // TMEM columns: S_A | S_B | O_A | O_B, P over S
+  __host__ __device__ static constexpr uint32_t s_col(int x) { return x ? 128u : 0u; }
+  __host__ __device__ static constexpr uint32_t o_col(int x) { return 256u + (x ? D : 0); }
+};
+static_assert(ChunkCfg<128>::kSmemBytes + 64 <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ float row_max(const float (&x)[kTile]) {
+  float m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = fmaxf(x[i], x[8 + i]);
+#pragma unroll
+  for (int e = 16; e < kTile; e += 16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmax3(m[i], x[e + i], x[e + 8 + i]);
+  }
+  return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+}
+
+template <int D, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
+  using C = ChunkCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + C::kKOff;
+  uint8_t* sV = smem + C::kVOff;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* q_full = bars;                 // [2]
+  uint64_t* q_empty = bars + 2;            // [2]
+  uint64_t* k_full = bars + 4;             // [kStages] K of a key tile has landed
+  uint64_t* v_full = k_full + kStages;     // V has landed
+  uint64_t* v_ready = v_full + kStages;    // V is free of values outside the unit's keys
+  uint64_t* kv_empty = v_ready + kStages;
+  uint64_t* s_full = kv_empty + kStages;   // [2]
+  uint64_t* p_half = s_full + 2;           // [2] P of keys 0-63 written
+  uint64_t* p_full = p_half + 2;           // [2]
+  uint64_t* o_full = p_full + 2;           // [2]
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ uint32_t missing[kStages];    // 16-key groups of a key tile whose page does not exist
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_half[x], kTile);
+      mbar_init(&p_full[x], kTile);
+      mbar_init(&o_full[x], 1);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_ready[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(&tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int* abort_v = &abort_flag;
+  grid_dependency_wait();                  // the list of work
+  grid_launch_dependents();
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    setmaxnreg_dec<kRegsControl>();
+    const int halves = D / 64, boxes = kTile / p.box;
+    const int box = lane / halves, sub = lane % halves;    // of a key tile: this lane's box
+    const bool loads = lane < boxes * halves;
+    const uint32_t box_off = sub * kSub + box * p.box * 128;
+    const int nowhere = p.a.num_pages * p.a.Hkv;           // a plane outside the maps: zeros
+    const uint32_t q_bytes = (uint32_t)(p.tile_tokens * p.a.G) * D * 2;
+    int qloads[2] = {0, 0};
+    int kv = 0;
+    bool ok = true;
+    Walk walk(p);
+    Piece pc;
+    while (ok && walk.next(p, pc)) {
+      const Half ha = half_of(p, pc, 0), hb = half_of(p, pc, 1);
+      const int lo = ha.lo, hi = hb.tokens > 0 ? hb.hi : ha.hi;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const Half& h = x ? hb : ha;
+        if (!ok || h.e <= h.a) continue;
+        if (qloads[x] > 0) ok = mbar_wait_bounded(&q_empty[x], (qloads[x] - 1) & 1, abort_v, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[x], q_bytes);
+          for (int c = 0; c < halves; ++c)
+            tma_load_3d(sQ + x * C::kTileBytes + c * kSub, &p.mq, &q_full[x], 64 * c, pc.hk * p.a.G,
+                        pc.en.row0 + h.tok0);
+        }
+        __syncwarp();
+        ++qloads[x];
+      }
+      const int32_t* table = p.a.block_table + (long long)pc.en.b * p.a.max_pages;
+      for (int j = pc.j0; ok && j < pc.j1; ++j, ++kv) {
+        const int st = kv % kStages;
+        const int key = pc.en.base + j * kTile + box * p.box;
+        int y = 0, z = nowhere;
+        uint32_t miss = 0;
+        if (loads && key < hi && key + p.box > lo) {
+          const int page = __ldg(table + key / p.a.page_size);
+          if (page >= 0 && page < p.a.num_pages) {
+            y = key % p.a.page_size;
+            z = page * p.a.Hkv + pc.hk;
+          } else {
+            miss = ((1u << (p.box / 16)) - 1) << (box * p.box / 16);
+          }
+        }
+        miss = __reduce_or_sync(0xffffffffu, miss);
+        if (kv >= kStages) ok = mbar_wait_bounded(&kv_empty[st], (kv / kStages - 1) & 1, abort_v, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          missing[st] = miss;
+          if (miss) atomicOr(p.a.err, kDevErrCheck);
+          mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
+          mbar_arrive_expect_tx(&v_full[st], C::kTileBytes);
+        }
+        __syncwarp();
+        if (loads) {
+          tma_load_3d(sK + st * C::kTileBytes + box_off, &p.mk, &k_full[st], 64 * sub, y, z);
+          tma_load_3d(sV + st * C::kTileBytes + box_off, &p.mv, &v_full[st], 64 * sub, y, z);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMAs
+    setmaxnreg_dec<kRegsControl>();
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
+      const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16);
+      const uint32_t k_lo = sdesc_lo(smem_u32(sK), 16);
+      const uint32_t v_lo = sdesc_lo(smem_u32(sV), kSub);
+      int qwaits[2] = {0, 0}, pwaits[2] = {0, 0};
+      int kv = 0;                          // ring position of key tile pc.j0
+      bool ok = true;
+      Walk walk(p);
+      Piece pc;
+      while (ok && walk.next(p, pc)) {
+        int a[2], e[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const Half h = half_of(p, pc, x);
+          a[x] = h.a;
+          e[x] = h.e;
+        }
+        auto issue_qk = [&](int x, int j) -> bool {
+          const int g = kv + j - pc.j0, st = g % kStages;
+          if (!mbar_wait_bounded(&k_full[st], (g / kStages) & 1, abort_v, kWaitLimitNs)) return false;
+          tc_fence_after();
+          const uint32_t qd = q_lo + x * (C::kTileBytes >> 4), kd = k_lo + st * (C::kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
+            umma_ss_lo(tmem + C::s_col(x), qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[x]);
+          if (j == e[x] - 1) umma_commit(&q_empty[x]);
+          return true;
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || e[x] <= a[x]) continue;
+          ok = mbar_wait_bounded(&q_full[x], qwaits[x]++ & 1, abort_v, kWaitLimitNs);
+        }
+        for (int j = pc.j0; ok && j < pc.j1; ++j) {
+          const int g = kv + j - pc.j0, st = g % kStages;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (ok && j == a[x] && a[x] < e[x]) ok = issue_qk(x, j);
+          if (!ok) break;
+          if (!mbar_wait_bounded(&v_ready[st], (g / kStages) & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
+          const bool any = (j >= a[0] && j < e[0]) || (j >= a[1] && j < e[1]);
+          if (!any) {                      // nobody reads the tile; its K must have landed too
+            ok = mbar_wait_bounded(&k_full[st], (g / kStages) & 1, abort_v, kWaitLimitNs);
+            mbar_arrive(&kv_empty[st]);
+            continue;
+          }
+          const uint32_t vd = v_lo + st * (C::kTileBytes >> 4);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j < a[x] || j >= e[x]) continue;
+            const uint32_t add = j > a[x] ? 1u : 0u;
+            if (!mbar_wait_bounded(&p_half[x], pwaits[x] & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kTile / 32; ++kk)
+              umma_ts_lo(tmem + C::o_col(x), tmem + C::s_col(x) + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
+                         kk > 0 ? 1u : add);
+            if (!mbar_wait_bounded(&p_full[x], pwaits[x] & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
+            ++pwaits[x];
+            tc_fence_after();
+#pragma unroll
+            for (int kk = kTile / 32; kk < kTile / 16; ++kk)
+              umma_ts_lo(tmem + C::o_col(x), tmem + C::s_col(x) + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv, 1u);
+            if (j == e[x] - 1) umma_commit(&o_full[x]);
+            else ok = issue_qk(x, j + 1);
+          }
+          umma_commit(&kv_empty[st]);
+        }
+        kv += pc.j1 - pc.j0;
+      }
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ values outside the unit's keys
+    setmaxnreg_dec<kRegsControl>();
+    int kv = 0;
+    bool ok = true;
+    Walk walk(p);
+    Piece pc;
+    while (ok && walk.next(p, pc)) {
+      const Half ha = half_of(p, pc, 0), hb = half_of(p, pc, 1);
+      const int lo = ha.lo, hi = hb.tokens > 0 ? hb.hi : ha.hi;
+      for (int j = pc.j0; j < pc.j1; ++j, ++kv) {
+        const int st = kv % kStages;
+        ok = mbar_wait_bounded(&v_full[st], (kv / kStages) & 1, abort_v, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int key0 = pc.en.base + j * kTile;
+        if (key0 < lo || key0 + kTile > hi) {
+          for (int i = lane; i < kTile * (D / 8); i += 32) {
+            const int row = i / (D / 8), c = i % (D / 8);
+            if (key0 + row < lo || key0 + row >= hi)       // a whole row: its swizzle does not matter
+              *reinterpret_cast<uint4*>(sV + st * C::kTileBytes + (c / 8) * kSub + row * 128 + (c % 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_ready[st]);
+      }
+    }
+  } else if (warp == 11) {
+    setmaxnreg_dec<kRegsControl>();
+  } else {
+    // ------------------------------------------------------------ softmax
+    setmaxnreg_inc<kRegsSoftmax>();
+    const int x = warp >> 2;
+    const int row = tid & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_addr = lane_base + C::s_col(x), o_addr = lane_base + C::o_col(x);
+    const int tok = row / p.a.G, head = row % p.a.G;
+    const float sl2 = p.scale_log2;
+    const float cap_l2 = p.a.softcap * kLog2e;
+    const float cap_in = CAP ? 2.f * sl2 / p.a.softcap : 0.f;
+    int it = 0, oc = 0, kv = 0;
+    bool ok = true;
+    Walk walk(p);
+    Piece pc;
+    while (ok && walk.next(p, pc)) {
+      const Half h = half_of(p, pc, x);
+      const int kv0_piece = kv;
+      kv += pc.j1 - pc.j0;
+      const bool whole = pc.j0 == 0 && pc.j1 == pc.en.tiles;
+      const bool row_valid = tok < h.tokens;             // rows behind the last token of the tile hold nothing
+      // partial results: slot 0 where the unit began in an earlier run, else slot 1
+      const long long part = ((long long)blockIdx.x * 2 + (pc.j0 == 0 ? 1 : 0)) * kUnitRows + x * kTile + row;
+      if (h.e <= h.a) {
+        if (!whole && row_valid) p.part_lse[part] = -INFINITY;
+        continue;
+      }
+      const int pos = pc.en.pos0 + h.tok0 + tok;
+      int klo = p.a.window < 0 ? 0 : max(0, pos - p.a.window);
+      int khi = min(pos + 1, pc.en.limit);
+      if (!row_valid) khi = klo = 0;
+      float m = -INFINITY, l = 0.f;
+      for (int j = h.a; j < h.e; ++j) {
+        const int g = kv0_piece + j - pc.j0;
+        if (!mbar_wait_bounded(&s_full[x], it & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
+        // the phase that published `missing` is over: this orders the read below after it
+        if (!mbar_wait_bounded(&k_full[g % kStages], (g / kStages) & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
+        const uint32_t miss = missing[g % kStages];
+        tc_fence_after();
+        uint32_t xr[kTile];
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) tmem_ld32(s_addr + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + ch * 32));
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(xr + ch * 32));
+        float s[kTile];
+#pragma unroll
+        for (int e = 0; e < kTile; ++e) {
+          s[e] = __uint_as_float(xr[e]);
+          if (CAP) s[e] = cap_l2 - 2.f * cap_l2 * rcp_approx(1.f + ex2_approx(s[e] * cap_in));
+        }
+        const int key0 = pc.en.base + j * kTile;
+        const int lo_t = klo - key0, hi_t = khi - key0;
+        uint32_t live = 0;                 // 32-column chunks with a key for any row of the warp
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+          if (__any_sync(0xffffffffu, lo_t < 32 * ch + 32 && hi_t > 32 * ch)) live |= 1u << ch;
+        const bool cut_lo = __any_sync(0xffffffffu, lo_t > 0);
+        const bool cut_hi = __any_sync(0xffffffffu, hi_t < kTile);
+        if (cut_lo && cut_hi) {
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) s[e] = (e >= lo_t && e < hi_t) ? s[e] : -INFINITY;
+        } else if (cut_lo) {
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) s[e] = (e >= lo_t) ? s[e] : -INFINITY;
+        } else if (cut_hi) {
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) s[e] = (e < hi_t) ? s[e] : -INFINITY;
+        }
+        if (miss) {
+#pragma unroll
+          for (int e = 0; e < kTile; ++e) s[e] = (miss >> (e / 16) & 1) ? -INFINITY : s[e];
+        }
+        const float mul = CAP ? 1.f : sl2;
+        const float m_new = fmaxf(m, row_max(s) * mul);
+        const bool need = (m == -INFINITY) ? (m_new > -INFINITY) : (m_new > m + kRescaleThreshold);
+        const bool rescale = __any_sync(0xffffffffu, need);
+        float alpha = 1.f;
+        if (rescale) {
+          alpha = (m == -INFINITY) ? 0.f : ex2_approx(m - m_new);
+          l *= alpha;
+          m = m_new;
+        }
+        const float neg_m = (m == -INFINITY) ? 0.f : -m;
+        if (rescale && j > h.a) {
+          // O is stable: its previous product was issued before this S, and they end in order
+#pragma unroll 1
+          for (int ch = 0; ch < D / 16; ++ch) {
+            uint32_t rr[16];
+            tmem_ld16(o_addr + ch * 16, rr);
+            tmem_wait_ld_dep16(rr);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+            tmem_st16(o_addr + ch * 16, rr);
+          }
+        }
+        float acc0 = 0.f, acc1 = 0.f, acc2 = 0.f, acc3 = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t pk[16];
+          if (!(live & (1u << ch))) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) pk[q] = 0u;
+          } else {
+#pragma unroll
+            for (int q = 0; q < 32; q += 4) {
+              const int e = ch * 32 + q;
+              float a0, a1, a2, a3;
+              ffma2(a0, a1, s[e], s[e + 1], mul, mul, neg_m, neg_m);
+              ffma2(a2, a3, s[e + 2], s[e + 3], mul, mul, neg_m, neg_m);
+              a0 = ex2_approx(a0);
+              a1 = ex2_approx(a1);
+              a2 = ex2_approx(a2);
+              a3 = ex2_approx(a3);
+              fadd2(acc0, acc1, acc0, acc1, a0, a1);
+              fadd2(acc2, acc3, acc2, acc3, a2, a3);
+              // P in bf16, the type of the product that follows; the sum keeps 32 bits
+              pk[q / 2] = pack_bf16x2(a0, a1);
+              pk[q / 2 + 1] = pack_bf16x2(a2, a3);
+            }
+          }
+          tmem_st16(s_addr + ch * 16, pk);
+          if (ch == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_half[x]);
+          }
+        }
+        l += (acc0 + acc1) + (acc2 + acc3);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[x]);
+        ++it;
+      }
+      if (!ok) break;
+
+      // ---------------------------------------------------------- epilogue
+      // O is read before this group's next p_half arrival, which the MMA warp waits for
+      // before it writes O again.
+      if (!mbar_wait_bounded(&o_full[x], oc & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
+      ++oc;
+      tc_fence_after();
+      const bool has = m != -INFINITY;
+      const float inv = has ? 1.f / l : 0.f;
+      const float lse = has ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      const long long out_row = (long long)(pc.en.row0 + h.tok0 + tok) * p.a.Hq + pc.hk * p.a.G + head;
+      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + out_row * D);
+      float4* po = reinterpret_cast<float4*>(p.part_o + part * D);
+#pragma unroll
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t rr[32];
+        tmem_ld32(o_addr + ch * 32, rr);
+        tmem_wait_ld_dep(rr);
+        if (row_valid && whole) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 v;
+            v.x = pack_bf16x2(__uint_as_float(rr[q * 8 + 0]) * inv, __uint_as_float(rr[q * 8 + 1]) * inv);
+            v.y = pack_bf16x2(__uint_as_float(rr[q * 8 + 2]) * inv, __uint_as_float(rr[q * 8 + 3]) * inv);
+            v.z = pack_bf16x2(__uint_as_float(rr[q * 8 + 4]) * inv, __uint_as_float(rr[q * 8 + 5]) * inv);
+            v.w = pack_bf16x2(__uint_as_float(rr[q * 8 + 6]) * inv, __uint_as_float(rr[q * 8 + 7]) * inv);
+            out[ch * 4 + q] = v;
+          }
+        } else if (row_valid) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            po[ch * 8 + q] = make_float4(__uint_as_float(rr[q * 4 + 0]) * inv, __uint_as_float(rr[q * 4 + 1]) * inv,
+                                         __uint_as_float(rr[q * 4 + 2]) * inv, __uint_as_float(rr[q * 4 + 3]) * inv);
+        }
+      }
+      if (row_valid && whole && p.a.lse) p.a.lse[out_row] = lse;
+      if (row_valid && !whole) p.part_lse[part] = lse;
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (abort_flag) {
+    // A bounded wait expired: report it, then give copies and MMAs still in flight time to
+    // land before TMEM and shared memory are released.
+    if (tid == 0) {
+      atomicOr(p.a.err, kDevErrTimeout);
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 2000000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the parts of a unit that cuts go through: block row c belongs to the first cut
+// inside its unit, one warp to a row; parts are added in the order of the keys.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+  constexpr int E = D / 32;
+  grid_dependency_wait();
+  const int c = blockIdx.x + 1;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const ChunkRun cut = p.runs[c];
+  if (!cut.inside) return;
+  const ChunkEntry en = p.entries[cut.entry];
+  const long long u0 = cut.step - cut.j, u1 = u0 + en.tiles;
+  if (p.runs[c - 1].step > u0) return;                    // not the first cut of its unit
+  const int x = r / kTile, row = r % kTile, tok = x * p.tile_tokens + row / p.a.G;
+  if (row >= p.tile_tokens * p.a.G || tok >= en.tokens) return;
+  float top = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int k = c - 1; k < p.num_runs && p.runs[k].step < u1; ++k) {
+    if (p.runs[k].step == p.runs[k + 1].step) continue;  // an empty run
+    const long long part = ((long long)k * 2 + (k == c - 1 ? 1 : 0)) * kUnitRows + r;
+    const float lse = p.part_lse[part];
+    if (lse == -INFINITY) continue;                      // no key in this part (a NaN goes on)
+    const float mx = fmaxf(top, lse);
+    const float keep = top == -INFINITY ? 0.f : ex2_approx((top - mx) * kLog2e), f = ex2_approx((lse - mx) * kLog2e);
+    top = mx;
+    l = l * keep + f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + f * p.part_o[part * D + lane + 32 * e];
+  }
+  const bool has = l != 0.f;
+  const float inv = has ? 1.f / l : 0.f;
+  const long long out_row = (long long)(en.row0 + tok) * p.a.Hq + cut.hk * p.a.G + row % p.a.G;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    static_cast<__nv_bfloat16*>(p.a.out)[out_row * D + lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
+  if (p.a.lse && lane == 0) p.a.lse[out_row] = has ? top + __log2f(l) * kLn2 : -INFINITY;
+}
+
+size_t up16(size_t x) { return (x + 15) / 16 * 16; }
+
+template <int D>
+cudaError_t launch_chunk(const ChunkParams& p, bool split, cudaStream_t s) {
+  chunk_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  auto kern = p.a.softcap > 0.f ? cache_chunk_kernel<D, true> : cache_chunk_kernel<D, false>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ChunkCfg<D>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.num_runs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = ChunkCfg<D>::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess || !split || p.num_runs < 2) return e;
+  cfg.gridDim = dim3(p.num_runs - 1, kUnitRows / 8);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<D>, p);
+}
+
+}  // namespace
+
+ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int max_len, int window) {
+  ChunkSplit t;
+  t.tile_tokens = kTile / G;
+  t.box = 16;
+  while (t.box < kTile && page_size % (2 * t.box) == 0) t.box *= 2;
+  const long long pair = 2LL * t.tile_tokens;
+  t.max_entries = (int)(T / pair + std::min<long long>(B, T));
+  // key tiles of a unit at most
+  const long long reach = window < 0 ? max_len : std::min<long long>(max_len, window + pair);
+  const long long tiles = (reach + t.box + kTile - 1) / kTile + 1;
+  t.runs = (int)std::min<long long>(148, std::max<long long>(1, (long long)t.max_entries * Hkv * tiles));
+  t.split = tiles > kShortUnit;
+  const size_t rows = t.split ? (size_t)t.runs * 2 * kUnitRows : 0;
+  t.bytes = sizeof(ChunkPlan) + up16((size_t)(B + 1) * 4) + up16((size_t)t.max_entries * sizeof(ChunkEntry)) +
+            up16((size_t)(t.runs + 1) * sizeof(ChunkRun)) + rows * (D + 1) * 4;
+  return t;
+}
+
+cudaError_t launch_cache_chunk(const CacheAttendParams& a, const ChunkSplit& t, void* workspace, cudaStream_t s) {
+  ChunkParams p = {};
+  const uint64_t e = 2;                    // bytes of an element
+  // strides of axes of length one are free: give the map one it accepts
+  const uint64_t qh = a.Hq > 1 ? (uint64_t)a.q_head * e : (uint64_t)a.D * e;
+  const uint64_t qt = a.T > 1 ? (uint64_t)a.q_token * e : (uint64_t)a.D * e;
+  const uint64_t row = (uint64_t)a.D * e, plane = (uint64_t)a.page_size * row;
+  if (!make_load_map(&p.mq, a.q, a.D, a.Hq, a.T, qh, qt, a.G, t.tile_tokens) ||
+      !make_load_map(&p.mk, a.k_pages, a.D, a.page_size, (uint64_t)a.num_pages * a.Hkv, row, plane, t.box, 1) ||
+      !make_load_map(&p.mv, a.v_pages, a.D, a.page_size, (uint64_t)a.num_pages * a.Hkv, row, plane, t.box, 1))
+    return cudaErrorInvalidValue;
+  char* ws = static_cast<char*>(workspace);
+  p.a = a;
+  p.plan = reinterpret_cast<ChunkPlan*>(ws);
+  ws += sizeof(ChunkPlan);
+  p.entry_first = reinterpret_cast<int*>(ws);
+  ws += up16((size_t)(a.B + 1) * 4);
+  p.entries = reinterpret_cast<ChunkEntry*>(ws);
+  ws += up16((size_t)t.max_entries * sizeof(ChunkEntry));
+  p.runs = reinterpret_cast<ChunkRun*>(ws);
+  ws += up16((size_t)(t.runs + 1) * sizeof(ChunkRun));
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_lse = p.part_o + (t.split ? (size_t)t.runs * 2 * kUnitRows * a.D : 0);
+  p.num_runs = t.runs;
+  p.tile_tokens = t.tile_tokens;
+  p.box = t.box;
+  p.max_entries = t.max_entries;
+  p.scale_log2 = a.scale * kLog2e;
+  return a.D == 64 ? launch_chunk<64>(p, t.split, s) : launch_chunk<128>(p, t.split, s);
+}
+
+}  // namespace swa

@@ -2,6 +2,7 @@
 // cache.  Internal to the library.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -46,5 +47,17 @@ struct TokenSplit {
 };
 TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach);
 cudaError_t launch_cache_token(CacheAttendParams p, const TokenSplit& t, void* workspace, cudaStream_t s);
+
+// The many-token kernel (bf16): how its work is laid out, from sizes only.
+struct ChunkSplit {
+  int runs;                         // blocks, each with an equal run of key tiles
+  int tile_tokens;                  // tokens of a query tile: 128 rows / heads of a group
+  int box;                          // keys of one load: they lie in one page
+  int max_entries;                  // token tiles of all sequences
+  bool split;                       // units long enough to be parted between blocks
+  size_t bytes;                     // workspace
+};
+ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int max_len, int window);
+cudaError_t launch_cache_chunk(const CacheAttendParams& p, const ChunkSplit& t, void* workspace, cudaStream_t s);
 
 }  // namespace swa

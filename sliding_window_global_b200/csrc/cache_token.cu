@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float x = s[mt][t][c];
-            if (CAP) x = cap_l2 - 2.f * cap_l2 * __frcp_rn(1.f + ex2_approx(x * cap_in));
+            if (CAP) x = cap_l2 - 2.f * cap_l2 * rcp_approx(1.f + ex2_approx(x * cap_in));
             else x *= sl2;
             if (masked) {
               const int key = key0 + 8 * t + 2 * (lane & 3) + (c & 1);

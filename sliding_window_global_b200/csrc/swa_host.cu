@@ -56,6 +56,20 @@ bool make_map(CUtensorMap* m, const void* base, int D, uint64_t rows, uint64_t p
   return r == CUDA_SUCCESS;
 }
 
+bool make_load_map(CUtensorMap* m, const void* base, int D, uint64_t dim_y, uint64_t dim_z, uint64_t stride_y_bytes,
+                   uint64_t stride_z_bytes, int box_y, int box_z) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || dim_y == 0 || dim_z == 0) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, dim_y, dim_z};
+  cuuint64_t strides[2] = {stride_y_bytes, stride_z_bytes};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_y, (cuuint32_t)box_z};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 swa_status validate_desc(const swa_plan_desc& d) {
   if (d.batch < 1 || d.seq_len < 1 || d.num_q_heads < 1 || d.num_kv_heads < 1 ||
       d.num_q_heads % d.num_kv_heads != 0 || d.max_global < 0 || d.num_side < 0 ||

@@ -60,6 +60,10 @@ bool make_map(CUtensorMap* m, const void* base, int D, uint64_t rows, uint64_t p
               uint64_t row_stride_bytes, uint64_t plane_stride_bytes, bool store_box = false,
               int box_rows = kTile);
 
+// 3-D bf16 TMA map for loads with the 128-byte swizzle, 64 columns by box_y by box_z.
+bool make_load_map(CUtensorMap* m, const void* base, int D, uint64_t dim_y, uint64_t dim_z, uint64_t stride_y_bytes,
+                   uint64_t stride_z_bytes, int box_y, int box_z);
+
 // Validate the arguments of one forward pass and enqueue it on `s`, with the
 // scratch `ws` and a persistent grid of `num_sms` CTAs.  *launches receives the
 // number of kernels enqueued.  In SWA_DEBUG_CHECKS mode the device check of

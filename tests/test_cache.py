@@ -65,7 +65,7 @@ ATTEND_BAD = [(dict(num_q_heads=3), INVALID), (dict(num_q_heads=0), INVALID), (d
               (dict(q=None), INVALID), (dict(out=_PTR + 4), INVALID), (dict(lse=_PTR + 1), INVALID),
               (dict(window=-2), INVALID), (dict(softcap=-1.0), INVALID), (dict(softcap=math.nan), INVALID),
               (dict(scale=math.inf), INVALID), (dict(max_len=-1), INVALID), (dict(q_stride0=4), INVALID),
-              (dict(q_stride1=-8), INVALID)]
+              (dict(q_stride1=-8), INVALID), (dict(q_stride0=0), INVALID)]
 
 
 @pytest.mark.parametrize("which,bad,status",
