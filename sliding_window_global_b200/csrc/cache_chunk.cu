@@ -220,20 +220,23 @@ __device__ __forceinline__ Half half_of(const ChunkParams& p, const Piece& pc, i
   return h;
 }
 
-// The pieces of a block's run, in order; every warp role walks them alike.
+// The pieces of a block's run, in order; every warp role walks them alike. The entry behind
+// a piece's own is fetched a piece ahead.
 struct Walk {
   long long left;
   int entry, hk, j;
+  ChunkEntry ahead;
   __device__ __forceinline__ Walk(const ChunkParams& p) {
     const ChunkRun& r = p.runs[blockIdx.x];
     left = p.runs[blockIdx.x + 1].step - r.step;
     entry = r.entry;
     hk = r.hk;
     j = r.j;
+    if (left > 0) ahead = p.entries[entry];
   }
   __device__ __forceinline__ bool next(const ChunkParams& p, Piece& pc) {
     if (left <= 0) return false;
-    pc.en = p.entries[entry];
+    pc.en = ahead;
     pc.hk = hk;
     pc.j0 = j;
     pc.j1 = (int)min((long long)pc.en.tiles, j + left);
@@ -242,6 +245,7 @@ struct Walk {
     if (++hk == p.a.Hkv) {
       hk = 0;
       ++entry;
+      if (left > 0) ahead = p.entries[entry];
     }
     return true;
   }
@@ -252,7 +256,8 @@ struct ChunkCfg {
   static constexpr uint32_t kTileBytes = 128u * D * 2u;
   static constexpr uint32_t kKOff = 2 * kTileBytes;
   static constexpr uint32_t kVOff = kKOff + kStages * kTileBytes;
-  static constexpr uint32_t kBarOff = kVOff + kStages * kTileBytes;
+  static constexpr uint32_t kOutOff = kVOff + kStages * kTileBytes;   // 4 KB a softmax warp: 32 rows x 64 columns
+  static constexpr uint32_t kBarOff = kOutOff + 8 * 4096;
   static constexpr int kNumBars = 2 + 2 + 4 * kStages + 2 + 2 + 2 + 2;
   static constexpr uint32_t kSmemBytes = kBarOff + kNumBars * 8 + 1024;
   static constexpr uint32_t kTmemCols = 512;
@@ -261,6 +266,10 @@ struct ChunkCfg {
   __host__ __device__ static constexpr uint32_t o_col(int x) { return 256u + (x ? D : 0); }
 };
 static_assert(ChunkCfg<128>::kSmemBytes + 64 <= 227 * 1024, "shared memory");
+
+// A value that is the same in every lane, said so to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ float row_max(const float (&x)[kTile]) {
   float m[8];
@@ -396,81 +405,93 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMAs
+    // The whole warp walks the steps and one thread issues, see elect_one.
     setmaxnreg_dec<kRegsControl>();
-    if (lane == 0) {
-      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
-      const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16);
-      const uint32_t k_lo = sdesc_lo(smem_u32(sK), 16);
-      const uint32_t v_lo = sdesc_lo(smem_u32(sV), kSub);
-      int qwaits[2] = {0, 0}, pwaits[2] = {0, 0};
-      int kv = 0;                          // ring position of key tile pc.j0
-      bool ok = true;
-      Walk walk(p);
-      Piece pc;
-      while (ok && walk.next(p, pc)) {
-        int a[2], e[2];
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
+    const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16);
+    const uint32_t k_lo = sdesc_lo(smem_u32(sK), 16);
+    const uint32_t v_lo = sdesc_lo(smem_u32(sV), kSub);
+    const uint32_t tm = uniform(tmem);
+    int qwaits[2] = {0, 0}, pwaits[2] = {0, 0};
+    int kv = 0;                            // ring position of the step
+    bool ok = true;
+    Walk walk(p);
+    Piece pc;
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_v, kWaitLimitNs));
+    };
+    auto issue_qk = [&](int x, int g, bool last) -> bool {
+      const int st = g % kStages;
+      if (!wait(&k_full[st], (g / kStages) & 1)) return false;
+      tc_fence_after();
+      const uint32_t qd = q_lo + x * (C::kTileBytes >> 4), kd = k_lo + st * (C::kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
+          umma_ss_lo(tm + C::s_col(x), qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[x]);
+        if (last) umma_commit(&q_empty[x]);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && walk.next(p, pc)) {
+      int a[2], e[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const Half h = half_of(p, pc, x);
+        a[x] = uniform(h.a);
+        e[x] = uniform(h.e);
+      }
+      const int j0 = uniform(pc.j0), j1 = uniform(pc.j1);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (!ok || e[x] <= a[x]) continue;
+        ok = wait(&q_full[x], qwaits[x]++ & 1);
+      }
+      for (int j = j0; ok && j < j1; ++j, ++kv) {
+        const int st = kv % kStages;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (ok && j == a[x] && a[x] < e[x]) ok = issue_qk(x, kv, j == e[x] - 1);
+        if (!ok) break;
+        if (!wait(&v_ready[st], (kv / kStages) & 1)) { ok = false; break; }
+        const bool any = (j >= a[0] && j < e[0]) || (j >= a[1] && j < e[1]);
+        if (!any) {                        // nobody reads the tile; its K must have landed too
+          ok = wait(&k_full[st], (kv / kStages) & 1);
+          if (lane == 0) mbar_arrive(&kv_empty[st]);
+          continue;
+        }
+        const uint32_t vd = v_lo + st * (C::kTileBytes >> 4);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const Half h = half_of(p, pc, x);
-          a[x] = h.a;
-          e[x] = h.e;
-        }
-        auto issue_qk = [&](int x, int j) -> bool {
-          const int g = kv + j - pc.j0, st = g % kStages;
-          if (!mbar_wait_bounded(&k_full[st], (g / kStages) & 1, abort_v, kWaitLimitNs)) return false;
+          if (!ok || j < a[x] || j >= e[x]) continue;
+          const uint32_t add = j > a[x] ? 1u : 0u;
+          if (!wait(&p_half[x], pwaits[x] & 1)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t qd = q_lo + x * (C::kTileBytes >> 4), kd = k_lo + st * (C::kTileBytes >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
-            umma_ss_lo(tmem + C::s_col(x), qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(&s_full[x]);
-          if (j == e[x] - 1) umma_commit(&q_empty[x]);
-          return true;
-        };
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || e[x] <= a[x]) continue;
-          ok = mbar_wait_bounded(&q_full[x], qwaits[x]++ & 1, abort_v, kWaitLimitNs);
-        }
-        for (int j = pc.j0; ok && j < pc.j1; ++j) {
-          const int g = kv + j - pc.j0, st = g % kStages;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (ok && j == a[x] && a[x] < e[x]) ok = issue_qk(x, j);
-          if (!ok) break;
-          if (!mbar_wait_bounded(&v_ready[st], (g / kStages) & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
-          const bool any = (j >= a[0] && j < e[0]) || (j >= a[1] && j < e[1]);
-          if (!any) {                      // nobody reads the tile; its K must have landed too
-            ok = mbar_wait_bounded(&k_full[st], (g / kStages) & 1, abort_v, kWaitLimitNs);
-            mbar_arrive(&kv_empty[st]);
-            continue;
-          }
-          const uint32_t vd = v_lo + st * (C::kTileBytes >> 4);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || j < a[x] || j >= e[x]) continue;
-            const uint32_t add = j > a[x] ? 1u : 0u;
-            if (!mbar_wait_bounded(&p_half[x], pwaits[x] & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
-            tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kTile / 32; ++kk)
-              umma_ts_lo(tmem + C::o_col(x), tmem + C::s_col(x) + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
-                         kk > 0 ? 1u : add);
-            if (!mbar_wait_bounded(&p_full[x], pwaits[x] & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
-            ++pwaits[x];
-            tc_fence_after();
+              umma_ts_lo(tm + C::o_col(x), tm + C::s_col(x) + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv, kk > 0 ? 1u : add);
+          }
+          __syncwarp();
+          if (!wait(&p_full[x], pwaits[x] & 1)) { ok = false; break; }
+          ++pwaits[x];
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int kk = kTile / 32; kk < kTile / 16; ++kk)
-              umma_ts_lo(tmem + C::o_col(x), tmem + C::s_col(x) + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv, 1u);
+              umma_ts_lo(tm + C::o_col(x), tm + C::s_col(x) + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv, 1u);
             if (j == e[x] - 1) umma_commit(&o_full[x]);
-            else ok = issue_qk(x, j + 1);
           }
-          umma_commit(&kv_empty[st]);
+          __syncwarp();
+          if (j < e[x] - 1) ok = issue_qk(x, kv + 1, j + 1 == e[x] - 1);
         }
-        kv += pc.j1 - pc.j0;
+        if (elect_one()) umma_commit(&kv_empty[st]);
+        __syncwarp();
       }
     }
   } else if (warp == 10) {
@@ -535,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       int klo = p.a.window < 0 ? 0 : max(0, pos - p.a.window);
       int khi = min(pos + 1, pc.en.limit);
       if (!row_valid) khi = klo = 0;
+      const int all_lo = __reduce_max_sync(0xffffffffu, klo);  // keys [all_lo, all_hi) need no mask in this warp
+      const int all_hi = __reduce_min_sync(0xffffffffu, khi);
       float m = -INFINITY, l = 0.f;
       for (int j = h.a; j < h.e; ++j) {
         const int g = kv0_piece + j - pc.j0;
@@ -560,8 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch)
           if (__any_sync(0xffffffffu, lo_t < 32 * ch + 32 && hi_t > 32 * ch)) live |= 1u << ch;
-        const bool cut_lo = __any_sync(0xffffffffu, lo_t > 0);
-        const bool cut_hi = __any_sync(0xffffffffu, hi_t < kTile);
+        const bool cut_lo = key0 < all_lo, cut_hi = key0 + kTile > all_hi;
         if (cut_lo && cut_hi) {
 #pragma unroll
           for (int e = 0; e < kTile; ++e) s[e] = (e >= lo_t && e < hi_t) ? s[e] : -INFINITY;
@@ -648,30 +670,52 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       const bool has = m != -INFINITY;
       const float inv = has ? 1.f / l : 0.f;
       const float lse = has ? (m + __log2f(l)) * kLn2 : -INFINITY;
-      const long long out_row = (long long)(pc.en.row0 + h.tok0 + tok) * p.a.Hq + pc.hk * p.a.G + head;
-      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + out_row * D);
-      float4* po = reinterpret_cast<float4*>(p.part_o + part * D);
+      // Rows leave through shared memory, so that eight lanes write 128 bytes of a row: 64 bf16
+      // or 32 fp32 columns at a time, the 16-byte chunks of a row swizzled by its number.
+      const int out_row = (pc.en.row0 + h.tok0 + tok) * p.a.Hq + pc.hk * p.a.G + head;
+      const int rows_here = min(h.tokens * p.a.G - (warp & 3) * 32, 32);       // rows of this warp that exist
+      uint8_t* stage = smem + C::kOutOff + warp * 4096;
+      const int sw_row = lane >> 3, sw_chunk = lane & 7;
 #pragma unroll
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t rr[32];
-        tmem_ld32(o_addr + ch * 32, rr);
-        tmem_wait_ld_dep(rr);
-        if (row_valid && whole) {
+      for (int half = 0; half < (whole ? D / 64 : D / 32); ++half) {
+        if (whole) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(rr[q * 8 + 0]) * inv, __uint_as_float(rr[q * 8 + 1]) * inv);
-            v.y = pack_bf16x2(__uint_as_float(rr[q * 8 + 2]) * inv, __uint_as_float(rr[q * 8 + 3]) * inv);
-            v.z = pack_bf16x2(__uint_as_float(rr[q * 8 + 4]) * inv, __uint_as_float(rr[q * 8 + 5]) * inv);
-            v.w = pack_bf16x2(__uint_as_float(rr[q * 8 + 6]) * inv, __uint_as_float(rr[q * 8 + 7]) * inv);
-            out[ch * 4 + q] = v;
+          for (int ch = 0; ch < 2; ++ch) {
+            uint32_t rr[32];
+            tmem_ld32(o_addr + half * 64 + ch * 32, rr);
+            tmem_wait_ld_dep(rr);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint4 v;
+              v.x = pack_bf16x2(__uint_as_float(rr[q * 8 + 0]) * inv, __uint_as_float(rr[q * 8 + 1]) * inv);
+              v.y = pack_bf16x2(__uint_as_float(rr[q * 8 + 2]) * inv, __uint_as_float(rr[q * 8 + 3]) * inv);
+              v.z = pack_bf16x2(__uint_as_float(rr[q * 8 + 4]) * inv, __uint_as_float(rr[q * 8 + 5]) * inv);
+              v.w = pack_bf16x2(__uint_as_float(rr[q * 8 + 6]) * inv, __uint_as_float(rr[q * 8 + 7]) * inv);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((ch * 4 + q) ^ (lane & 7)) << 4)) = v;
+            }
           }
-        } else if (row_valid) {
+        } else {
+          uint32_t rr[32];
+          tmem_ld32(o_addr + half * 32, rr);
+          tmem_wait_ld_dep(rr);
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            po[ch * 8 + q] = make_float4(__uint_as_float(rr[q * 4 + 0]) * inv, __uint_as_float(rr[q * 4 + 1]) * inv,
+          for (int q = 0; q < 8; ++q) {
+            const float4 v = make_float4(__uint_as_float(rr[q * 4 + 0]) * inv, __uint_as_float(rr[q * 4 + 1]) * inv,
                                          __uint_as_float(rr[q * 4 + 2]) * inv, __uint_as_float(rr[q * 4 + 3]) * inv);
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = v;
+          }
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + sw_row;
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((sw_chunk ^ (r & 7)) << 4));
+          const int to = __shfl_sync(0xffffffffu, out_row, r);
+          uint4* dst = whole ? reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + (long long)to * D) + half * 8
+                             : reinterpret_cast<uint4*>(p.part_o + (part - lane + r) * D) + half * 8;
+          if (r < rows_here) dst[sw_chunk] = v;
+        }
+        __syncwarp();
       }
       if (row_valid && whole && p.a.lse) p.a.lse[out_row] = lse;
       if (row_valid && !whole) p.part_lse[part] = lse;

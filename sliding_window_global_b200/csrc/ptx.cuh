@@ -120,6 +120,20 @@ __device__ __forceinline__ bool wait_count_bounded(const unsigned* count, unsign
   return true;
 }
 
+// ---------------------------------------------------------------- one thread of a warp
+// True in one thread of a converged warp.  Code that the whole warp reaches with uniform
+// values, and in which one thread issues, keeps those values in uniform registers, which
+// tcgen05.mma takes its operands from.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
