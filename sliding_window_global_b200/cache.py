@@ -11,7 +11,7 @@ from typing import Optional
 import torch
 
 from .rotary import (_NO_ROTATION, F, I, I64, P, HeadNorm, Rotary, Rotation, check_index, check_rows,
-                     current_stream, head_norm, on_device)
+                     current_stream, elsewhere, head_norm)
 from .swa import SwaError, _dtype_code, load_library
 
 
@@ -74,25 +74,27 @@ class PagedCache:
         self._error = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
         self._cache = Cache(k_pages.data_ptr(), v_pages.data_ptr(), pages, self.num_kv_heads, self.page_size,
                             self.head_dim, _dtype_code(self.dtype), self._error.data_ptr())
+        self._ref = ctypes.byref(self._cache)
+        self._device = k_pages.device
 
     def _rows(self, t, name, T=None, heads=None):
-        check_rows(t, name, self.k_pages, 3, self.dtype)
-        if t.shape[2] != self.head_dim or (T is not None and t.shape[0] != T) or \
-                (heads is not None and t.shape[1] != heads):
+        strides = check_rows(t, name, self._device, 3, self.dtype)
+        n, h, d = t.shape
+        if d != self.head_dim or (T is not None and n != T) or (heads is not None and h != heads):
             raise ValueError(f"{name} must be [{'T' if T is None else T}, {'heads' if heads is None else heads}, "
                              f"{self.head_dim}], got {tuple(t.shape)}")
+        return strides
 
     def _batch(self, T, seq_lens, block_table, cu_tokens) -> CacheBatch:
         B = seq_lens.shape[0]
         if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1:
             raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
-        if cu_tokens is None and (B == 0 or T % B):
-            if T or B:
-                raise ValueError(f"{T} rows cannot be shared by {B} sequences; pass cu_tokens")
-        like = self.k_pages
-        return CacheBatch(B, T, check_index(block_table, "block_table", like, block_table.shape),
-                          block_table.shape[1], check_index(seq_lens, "seq_lens", like, (B,)),
-                          check_index(cu_tokens, "cu_tokens", like, (B + 1,)))
+        if cu_tokens is None and (T or B) and (B == 0 or T % B):
+            raise ValueError(f"{T} rows cannot be shared by {B} sequences; pass cu_tokens")
+        device = self._device
+        return CacheBatch(B, T, check_index(block_table, "block_table", device, block_table.shape),
+                          block_table.shape[1], check_index(seq_lens, "seq_lens", device, (B,)),
+                          check_index(cu_tokens, "cu_tokens", device, (B + 1,)))
 
     def append(self, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, *,
                q: Optional[torch.Tensor] = None, cu_tokens: Optional[torch.Tensor] = None,
@@ -103,34 +105,36 @@ class PagedCache:
         the pages, k normed (``norm_eps``, as in ``Rotary.forward``) and rotated at its
         position; q [T, Hq, D] is normed and rotated alike into ``q_out``, which is returned
         (it may be q; rows of no sequence are not written)."""
+        ctx = elsewhere(self.k_pages, "k_pages", stream)
+        if ctx is None:
+            return self._append(k, v, seq_lens, block_table, q, cu_tokens, rotary, norm_eps, q_weight, k_weight, q_out)
+        with ctx:
+            return self._append(k, v, seq_lens, block_table, q, cu_tokens, rotary, norm_eps, q_weight, k_weight, q_out)
+
+    def _append(self, k, v, seq_lens, block_table, q, cu_tokens, rotary, norm_eps, q_weight, k_weight, q_out):
+        ks = self._rows(k, "k", heads=self.num_kv_heads)
         T = k.shape[0]
-        self._rows(k, "k", heads=self.num_kv_heads)
-        self._rows(v, "v", T, self.num_kv_heads)
+        vs = self._rows(v, "v", T, self.num_kv_heads)
         if rotary is not None and rotary.head_dim != self.head_dim:
             raise ValueError(f"the rotation is for head_dim {rotary.head_dim}, the cache's is {self.head_dim}")
-        Hq = 0
-        if q is not None:
-            self._rows(q, "q", T)
+        Hq, qs, os, q_ptr, qo_ptr = 0, (0, 0), (0, 0), None, None
+        if q is None:
+            q_out = None
+        else:
+            qs = self._rows(q, "q", T)
             Hq = q.shape[1]
-        with on_device(self.k_pages, stream):
-            qs = os = (0, 0)
-            if q is None:
-                q_out = None
+            if q_out is None:
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+                os = (Hq * self.head_dim, self.head_dim)
             else:
-                if q_out is None:
-                    q_out = torch.empty((T, Hq, self.head_dim), dtype=self.dtype, device=self.k_pages.device)
-                else:
-                    self._rows(q_out, "q_out", T, Hq)
-                qs, os = q.stride(), q_out.stride()
-            ks, vs = k.stride(), v.stride()
-            batch = self._batch(T, seq_lens, block_table, cu_tokens)
-            a = CacheAppendArgs(
-                Hq, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1],
-                vs[0], vs[1], None if q is None else q_out.data_ptr(), os[0], os[1],
-                _NO_ROTATION if rotary is None else rotary.struct,
-                head_norm(norm_eps, q_weight, k_weight, self.head_dim, self.k_pages))
-            st = self._lib.swa_cache_append(ctypes.byref(self._cache), ctypes.byref(batch), ctypes.byref(a),
-                                            current_stream())
+                os = self._rows(q_out, "q_out", T, Hq)
+            q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
+        batch = self._batch(T, seq_lens, block_table, cu_tokens)
+        a = CacheAppendArgs(
+            Hq, q_ptr, k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qo_ptr, os[0], os[1],
+            _NO_ROTATION if rotary is None else rotary.struct,
+            head_norm(norm_eps, q_weight, k_weight, self.head_dim, self._device))
+        st = self._lib.swa_cache_append(self._ref, ctypes.byref(batch), ctypes.byref(a), current_stream(self.k_pages))
         if st != 0:
             raise SwaError(st, "swa_cache_append")
         return q_out
@@ -147,39 +151,50 @@ class PagedCache:
         capacity).  ``softcap`` c > 0 turns a score s into ``c tanh(s / c)``; scale 0 is
         1/sqrt(D).  Returns ``(out, lse)``: [T, Hq, D] and fp32 [T, Hq] (natural log); rows of
         no sequence are not written."""
-        self._rows(q, "q")
+        ctx = elsewhere(self.k_pages, "k_pages", stream)
+        args = (q, seq_lens, block_table, cu_tokens, max_tokens, max_len, window, softcap, scale, out, lse, return_lse)
+        if ctx is None:
+            return self._attend(*args)
+        with ctx:
+            return self._attend(*args)
+
+    def _attend(self, q, seq_lens, block_table, cu_tokens, max_tokens, max_len, window, softcap, scale, out, lse,
+                return_lse):
+        qs = self._rows(q, "q")
         T, Hq, D = q.shape
-        if window is not None and window < 0:
+        if window is None:
+            window = -1
+        elif window < 0:
             raise ValueError("window must be None or at least 0")
-        with on_device(self.k_pages, stream):
-            batch = self._batch(T, seq_lens, block_table, cu_tokens)
-            if out is None:
-                out = torch.empty((T, Hq, D), dtype=self.dtype, device=q.device)
-            else:
-                self._rows(out, "out", T, Hq)
-                if not out.is_contiguous():
-                    raise ValueError("out must be contiguous")
-            if lse is None:
-                if return_lse:
-                    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-            elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous() or \
-                    lse.device != q.device:
-                raise ValueError(f"lse must be a contiguous fp32 [{T}, {Hq}] on {q.device}")
-            qs = q.stride()
-            a = CacheAttendArgs(Hq, q.data_ptr(), qs[0], qs[1], T if max_tokens is None else int(max_tokens),
-                                int(max_len), -1 if window is None else int(window), float(softcap), float(scale),
-                                out.data_ptr(), None if lse is None else lse.data_ptr(), None, 0)
-            refs = ctypes.byref(self._cache), ctypes.byref(batch), ctypes.byref(a)
-            need = self._lib.swa_cache_attend_workspace_bytes(*refs)
-            if need:
-                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-                a.workspace, a.workspace_bytes = ws.data_ptr(), need
-            st = self._lib.swa_cache_attend(*refs, current_stream())
+        batch = self._batch(T, seq_lens, block_table, cu_tokens)
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            self._rows(out, "out", T, Hq)
+            if not out.is_contiguous():
+                raise ValueError("out must be contiguous")
+        if lse is None:
+            if return_lse:
+                lse = torch.empty((T, Hq), dtype=torch.float32, device=self._device)
+        elif lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous() or \
+                lse.device != self._device:
+            raise ValueError(f"lse must be a contiguous fp32 [{T}, {Hq}] on {self._device}")
+        a = CacheAttendArgs(Hq, q.data_ptr(), qs[0], qs[1], T if max_tokens is None else max_tokens, max_len, window,
+                            softcap, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), None, 0)
+        refs = self._ref, ctypes.byref(batch), ctypes.byref(a)
+        need = self._lib.swa_cache_attend_workspace_bytes(*refs)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=self._device)
+            a.workspace, a.workspace_bytes = ws.data_ptr(), need
+        st = self._lib.swa_cache_attend(*refs, current_stream(self.k_pages))
         if st != 0:
             raise SwaError(st, "swa_cache_attend")
         return out, lse
 
     def check(self, stream=None) -> int:
         """Synchronise, read and clear the cache's error word (0 = OK)."""
-        with on_device(self.k_pages, stream):
-            return int(self._lib.swa_cache_check(ctypes.byref(self._cache), current_stream()))
+        ctx = elsewhere(self.k_pages, "k_pages", stream)
+        if ctx is None:
+            return int(self._lib.swa_cache_check(self._ref, current_stream(self.k_pages)))
+        with ctx:
+            return int(self._lib.swa_cache_check(self._ref, current_stream(self.k_pages)))

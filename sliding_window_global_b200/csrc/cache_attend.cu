@@ -248,10 +248,9 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
 // ------------------------------------------------------------------ launches
 template <int D>
 cudaError_t launch_core(const CacheAttendParams& p, int row_tiles, cudaStream_t s) {
-  auto kern = cache_core_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, core_smem_bytes<D>());
+  cudaError_t e = allow_smem<&cache_core_kernel<D>>(core_smem_bytes<D>());
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)((long long)p.B * row_tiles * p.nsplit), p.Hkv), kCoreThreads, core_smem_bytes<D>(), s>>>(
+  cache_core_kernel<D><<<dim3((unsigned)((long long)p.B * row_tiles * p.nsplit), p.Hkv), kCoreThreads, core_smem_bytes<D>(), s>>>(
       p, row_tiles);
   return cudaGetLastError();
 }
@@ -401,6 +400,7 @@ swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (sp.kernel == swa::AttendSplit::kToken) {
+    if (!sp.token.ok) return SWA_ERR_UNSUPPORTED;
     e = swa::launch_cache_token(p, sp.token, a->workspace, s);
     return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
   }

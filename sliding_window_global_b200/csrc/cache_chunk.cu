@@ -58,17 +58,10 @@ struct ChunkRun {
   int inside;                      // the cut goes through a unit
 };
 
-struct ChunkPlan {
-  int entries;
-  int pad;
-  long long steps;
-};
-
 struct ChunkParams {
   CUtensorMap mq, mk, mv;
   CacheAttendParams a;
-  ChunkPlan* plan;
-  int* entry_first;                // [B + 1] first entry of each sequence
+  int* entry_first;                // [B] first entry of each sequence (many sequences)
   ChunkEntry* entries;
   ChunkRun* runs;                  // [runs + 1]
   float* part_o;                   // [runs, 2, 256, D]
@@ -100,12 +93,17 @@ __device__ __forceinline__ long long block_scan(long long x, long long* warp_sum
   return x + before;
 }
 
+// The first kPlanThreads sequences and entries are searched in shared memory, more of them
+// in the workspace.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkParams p) {
-  __shared__ long long warp_sums[kPlanThreads / 32];
+  __shared__ long long warp_sums[kPlanThreads / 32], s_step[kPlanThreads];
+  __shared__ int s_entry[kPlanThreads + 1], s_tiles[kPlanThreads];
   const CacheAttendParams& a = p.a;
   const int pair = 2 * p.tile_tokens;
   grid_launch_dependents();
   // token tile pairs of each sequence
+  const bool few = a.B <= kPlanThreads;
+  int* entry_first = few ? s_entry : p.entry_first;
   long long total, before = 0;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
@@ -116,11 +114,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       n = (s.count + pair - 1) / pair;
     }
     const long long upto = block_scan(n, warp_sums, total);
-    if (b < a.B) p.entry_first[b] = (int)min(before + upto - n, (long long)p.max_entries);
+    if (b < a.B) entry_first[b] = (int)min(before + upto - n, (long long)p.max_entries);
     before += total;
   }
   const int entries = (int)min(before, (long long)p.max_entries);   // overlapping cu_tokens may name more rows than T
-  if (threadIdx.x == 0) p.entry_first[a.B] = entries;
   __syncthreads();
   // their keys, and the first step of each
   long long steps = 0;
@@ -132,11 +129,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       int lo = 0, hi = a.B - 1;                          // the last sequence that starts at or before e
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.entry_first[mid] <= e) lo = mid;
+        if (entry_first[mid] <= e) lo = mid;
         else hi = mid - 1;
       }
       const CacheSeq s = cache_seq(a, lo);
-      const int t0 = (e - p.entry_first[lo]) * pair;
+      const int t0 = (e - entry_first[lo]) * pair;
       r.b = lo;
       r.row0 = s.from + t0;
       r.tokens = min(pair, s.count - t0);
@@ -150,14 +147,15 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
     const long long upto = block_scan(n, warp_sums, total);
     r.first = steps + upto - n;
     if (e < entries) p.entries[e] = r;
+    if (e0 == 0) {
+      s_step[threadIdx.x] = r.first;
+      s_tiles[threadIdx.x] = r.tiles;
+    }
     steps += total;
-  }
-  if (threadIdx.x == 0) {
-    p.plan->entries = entries;
-    p.plan->steps = steps;
   }
   __syncthreads();
   // equal runs, their cuts moved to a unit's edge where the unit is short or the edge near
+  const bool listed = entries <= kPlanThreads;
   for (int c = threadIdx.x; c <= p.num_runs; c += kPlanThreads) {
     const long long x = steps * c / p.num_runs;
     ChunkRun r = {x, entries, 0, 0, 0};
@@ -165,20 +163,21 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       int lo = 0, hi = entries - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.entries[mid].first <= x) lo = mid;
+        if ((listed ? s_step[mid] : p.entries[mid].first) <= x) lo = mid;
         else hi = mid - 1;
       }
-      const ChunkEntry& en = p.entries[lo];
+      const int tiles = listed ? s_tiles[lo] : p.entries[lo].tiles;
+      const long long in = x - (listed ? s_step[lo] : p.entries[lo].first);
       r.entry = lo;
-      r.hk = (int)((x - en.first) / en.tiles);
-      r.j = (int)((x - en.first) % en.tiles);
-      const bool to_start = en.tiles <= kShortUnit ? 2 * r.j < en.tiles : r.j < kMinPiece;
-      const bool to_end = en.tiles <= kShortUnit ? !to_start : en.tiles - r.j < kMinPiece;
+      r.hk = (int)(in / tiles);
+      r.j = (int)(in % tiles);
+      const bool to_start = tiles <= kShortUnit ? 2 * r.j < tiles : r.j < kMinPiece;
+      const bool to_end = tiles <= kShortUnit ? !to_start : tiles - r.j < kMinPiece;
       if (to_start) {
         r.step -= r.j;
         r.j = 0;
       } else if (to_end) {
-        r.step += en.tiles - r.j;
+        r.step += tiles - r.j;
         r.j = 0;
         if (++r.hk == a.Hkv) {
           r.hk = 0;
@@ -766,19 +765,26 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
     const long long part = ((long long)k * 2 + (k == c - 1 ? 1 : 0)) * kUnitRows + r;
     const float lse = p.part_lse[part];
     if (lse == -INFINITY) continue;                      // no key in this part (a NaN goes on)
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(p.part_o + part * D + lane * 2 + 64 * (e / 2));
+      x[e] = v.x;
+      x[e + 1] = v.y;
+    }
     const float mx = fmaxf(top, lse);
     const float keep = top == -INFINITY ? 0.f : ex2_approx((top - mx) * kLog2e), f = ex2_approx((lse - mx) * kLog2e);
     top = mx;
     l = l * keep + f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + f * p.part_o[part * D + lane + 32 * e];
+    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + f * x[e];
   }
   const bool has = l != 0.f;
   const float inv = has ? 1.f / l : 0.f;
   const long long out_row = (long long)(en.row0 + tok) * p.a.Hq + cut.hk * p.a.G + row % p.a.G;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.a.out) + out_row * D) + lane;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    static_cast<__nv_bfloat16*>(p.a.out)[out_row * D + lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
+  for (int e = 0; e < E; e += 2) out[16 * e] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
   if (p.a.lse && lane == 0) p.a.lse[out_row] = has ? top + __log2f(l) * kLn2 : -INFINITY;
 }
 
@@ -789,9 +795,11 @@ cudaError_t launch_chunk(const ChunkParams& p, bool split, cudaStream_t s) {
   chunk_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto kern = p.a.softcap > 0.f ? cache_chunk_kernel<D, true> : cache_chunk_kernel<D, false>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ChunkCfg<D>::kSmemBytes);
+  const bool cap = p.a.softcap > 0.f;
+  e = cap ? allow_smem<&cache_chunk_kernel<D, true>>((int)ChunkCfg<D>::kSmemBytes)
+          : allow_smem<&cache_chunk_kernel<D, false>>((int)ChunkCfg<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
+  auto kern = cap ? cache_chunk_kernel<D, true> : cache_chunk_kernel<D, false>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -825,7 +833,7 @@ ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int m
   t.runs = (int)std::min<long long>(148, std::max<long long>(1, (long long)t.max_entries * Hkv * tiles));
   t.split = tiles > kShortUnit;
   const size_t rows = t.split ? (size_t)t.runs * 2 * kUnitRows : 0;
-  t.bytes = sizeof(ChunkPlan) + up16((size_t)(B + 1) * 4) + up16((size_t)t.max_entries * sizeof(ChunkEntry)) +
+  t.bytes = up16((size_t)B * 4) + up16((size_t)t.max_entries * sizeof(ChunkEntry)) +
             up16((size_t)(t.runs + 1) * sizeof(ChunkRun)) + rows * (D + 1) * 4;
   return t;
 }
@@ -843,10 +851,8 @@ cudaError_t launch_cache_chunk(const CacheAttendParams& a, const ChunkSplit& t, 
     return cudaErrorInvalidValue;
   char* ws = static_cast<char*>(workspace);
   p.a = a;
-  p.plan = reinterpret_cast<ChunkPlan*>(ws);
-  ws += sizeof(ChunkPlan);
   p.entry_first = reinterpret_cast<int*>(ws);
-  ws += up16((size_t)(a.B + 1) * 4);
+  ws += up16((size_t)a.B * 4);
   p.entries = reinterpret_cast<ChunkEntry*>(ws);
   ws += up16((size_t)t.max_entries * sizeof(ChunkEntry));
   p.runs = reinterpret_cast<ChunkRun*>(ws);

@@ -6,9 +6,23 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/swa.h"
 
 namespace swa {
+
+// Allow Kern `bytes` of dynamic shared memory; asked of the driver once a device.
+template <auto Kern>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load() >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+  return e;
+}
 
 // Checks of a cache and of a batch: SWA_ERR_INVALID_ARG for a null or misaligned pointer
 // or a bad size, SWA_ERR_UNSUPPORTED for a shape the kernels do not implement.
@@ -27,7 +41,7 @@ struct CacheAttendParams {
   int* err;
   float* part_o;                    // partial results, each the softmax over its own keys
   float* part_lse;
-  void* prefix;                     // few-token kernel: [B + 1] int64 first steps of the sequences
+  int* prefix;                      // few-token kernel: [B + 1] first steps of the sequences
   long long q_token, q_head;        // strides of q, elements
   int B, T, Hq, Hkv, G, D;
   int num_pages, page_size, max_pages;
@@ -43,6 +57,7 @@ constexpr int kTokenRows = 32;
 struct TokenSplit {
   int warps, blocks;                // warps of a block, blocks
   int row_pad;                      // rows of a partial result
+  bool ok;                          // the steps can be counted in 31 bits
   size_t bytes;                     // workspace
 };
 TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach);

@@ -83,24 +83,25 @@ __device__ __forceinline__ TokenUnit token_unit(const CacheAttendParams& p, int 
   return u;
 }
 
-// Sum of the steps of all units, by one warp; each lane calls each(b, the first step of
-// sequence b's units, their number, whether something of b's bounds does not hold).
+// Sum of the steps of all units, by one warp (below 2^31, checked on the host); each lane
+// calls each(b, the first step of sequence b's units, their number, whether something of b's
+// bounds does not hold).
 template <int D, typename F>
-__device__ __forceinline__ long long scan_steps(const CacheAttendParams& p, int lane, F each) {
-  long long before = 0;
+__device__ __forceinline__ int scan_steps(const CacheAttendParams& p, int lane, F each) {
+  int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    long long mine = 0;
+    int mine = 0;
     bool bad = false;
     if (b < p.B) {
       const TokenUnit u = token_unit<D>(p, b);
-      mine = (long long)u.steps * p.Hkv;
+      mine = u.steps * p.Hkv;
       bad = u.s.bad;
     }
-    long long sum = mine;
+    int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, sum, o);
+      const int up = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += up;
     }
     each(b, before + sum - mine, mine, bad);
@@ -109,8 +110,16 @@ __device__ __forceinline__ long long scan_steps(const CacheAttendParams& p, int 
   return before;
 }
 
-// Run of warp w of W over n steps: [run_begin(w), run_begin(w + 1)).
-__device__ __forceinline__ long long run_begin(long long n, int w, int W) { return n * w / W; }
+// The runs of W warps over n steps: the first n % W of n / W + 1 steps, the rest of n / W.
+struct Runs {
+  int each, extra;
+  __device__ __forceinline__ Runs(int n, int W) : each(n / W), extra(n % W) {}
+  __device__ __forceinline__ int begin(int w) const { return w * each + min(w, extra); }
+  __device__ __forceinline__ int of(int step) const {    // the run that holds a step
+    const int head = extra * (each + 1);
+    return step < head ? step / (each + 1) : extra + (step - head) / each;
+  }
+};
 
 template <int D, int MT, bool CAP>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __grid_constant__ CacheAttendParams p) {
@@ -124,32 +133,35 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
   grid_launch_dependents();
 
   // ---- this warp's run, and the sequence, head and step it starts at
-  long long* prefix = reinterpret_cast<long long*>(p.prefix);
-  const long long n = scan_steps<D>(p, lane, [&](int b, long long first, long long, bool bad) {
+  int last_first = 0, last_mine = 0;       // of the last 32 sequences: with B <= 32, of all
+  const int n = scan_steps<D>(p, lane, [&](int b, int first, int mine, bool bad) {
+    last_first = first;
+    last_mine = mine;
     if (w != 0 || b >= p.B) return;
-    prefix[b] = first;
+    p.prefix[b] = first;
     if (bad) atomicOr(p.err, kDevErrCheck);
   });
-  if (w == 0 && lane == 0) prefix[p.B] = n;
-  const long long begin = run_begin(n, w, W);
-  const int total = (int)(run_begin(n, w + 1, W) - begin);
+  if (w == 0 && lane == 0) p.prefix[p.B] = n;
+  const Runs runs(n, W);
+  const int begin = runs.begin(w);
+  const int total = runs.begin(w + 1) - begin;
   if (total == 0) return;
   int b = 0, hk = 0, j = 0;
   {
-    int fb = 0;
-    long long ff = 0;
-    scan_steps<D>(p, lane, [&](int bb, long long first, long long mine, bool) {
-      const unsigned hit = __ballot_sync(0xffffffffu, bb < p.B && first <= begin && begin < first + mine);
+    int first = 0, steps = 1;
+    auto look = [&](int bb, int ff, int mine, bool) {
+      const unsigned hit = __ballot_sync(0xffffffffu, ff <= begin && begin < ff + mine);
       if (hit) {
         const int src = __ffs(hit) - 1;
-        fb = __shfl_sync(0xffffffffu, bb, src);
-        ff = __shfl_sync(0xffffffffu, first, src);
+        b = __shfl_sync(0xffffffffu, bb, src);
+        first = __shfl_sync(0xffffffffu, ff, src);
+        steps = __shfl_sync(0xffffffffu, mine, src) / p.Hkv;
       }
-    });
-    const int steps = token_unit<D>(p, fb).steps;
-    b = fb;
-    hk = (int)((begin - ff) / steps);
-    j = (int)((begin - ff) % steps);
+    };
+    if (p.B <= 32) look(lane, last_first, last_mine, false);
+    else scan_steps<D>(p, lane, look);
+    hk = (begin - first) / steps;
+    j = (begin - first) % steps;
   }
 
   // ---- fetching side: its own place in the list, kStages - 1 steps ahead
@@ -410,29 +422,20 @@ __global__ void __launch_bounds__(128) cache_token_merge_kernel(const __grid_con
   const int r = blockIdx.x % max_rows;
   const int hk = blockIdx.x / max_rows % p.Hkv;
   const int b = blockIdx.x / max_rows / p.Hkv;
-  const long long* prefix = reinterpret_cast<const long long*>(p.prefix);
-  const long long first = prefix[b], steps = (prefix[b + 1] - first) / p.Hkv, n = prefix[p.B];
-  if (steps == 0) return;
   const CacheSeq s = cache_seq(p, b);
-  if (r >= s.count * p.G) return;
-  const long long u0 = first + hk * steps, u1 = u0 + steps;
-  // the runs that hold the unit's first and last step
-  auto run_of = [&](long long step) {
-    int w = (int)(step * W / n);
-    while (w + 1 < W && run_begin(n, w + 1, W) <= step) ++w;
-    while (run_begin(n, w, W) > step) --w;
-    return w;
-  };
-  const int w0 = run_of(u0), w1 = run_of(u1 - 1);
+  const int first = p.prefix[b], steps = (p.prefix[b + 1] - first) / p.Hkv, n = p.prefix[p.B];
+  if (steps == 0 || r >= s.count * p.G) return;
+  const int u0 = first + hk * steps, u1 = u0 + steps;
+  // the runs that hold the unit's first and last step (none between them is empty)
+  const Runs runs(n, W);
+  const int w0 = runs.of(u0), w1 = runs.of(u1 - 1);
   if (w0 == w1) return;                    // stored whole
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll 4
   for (int w = w0 + wp; w <= w1; w += 4) {
-    const long long at = run_begin(n, w, W);
-    if (at == run_begin(n, w + 1, W)) continue;          // an empty run (fewer steps than warps)
-    const long long row = (2LL * w + (at <= u0 ? 1 : 0)) * row_pad + r;
+    const long long row = (2LL * w + (w == w0 ? 1 : 0)) * row_pad + r;
     const float lse = p.part_lse[row];
     float x[E];
 #pragma unroll
@@ -471,12 +474,9 @@ __global__ void __launch_bounds__(128) cache_token_merge_kernel(const __grid_con
 
 template <int D, int MT, bool CAP>
 cudaError_t launch_token(const CacheAttendParams& p, const TokenSplit& t, cudaStream_t s) {
-  auto kern = cache_token_kernel<D, MT, CAP>;
-  const int smem = t.warps * kStages * Step<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMaxWarps * kStages * Step<D>::kBytes);
+  cudaError_t e = allow_smem<&cache_token_kernel<D, MT, CAP>>(kMaxWarps * kStages * Step<D>::kBytes);
   if (e != cudaSuccess) return e;
-  kern<<<t.blocks, t.warps * 32, smem, s>>>(p);
+  cache_token_kernel<D, MT, CAP><<<t.blocks, t.warps * 32, t.warps * kStages * Step<D>::kBytes, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -503,13 +503,14 @@ TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach) {
   t.warps = 1;
   while (t.warps < kMaxWarps && 148 * t.warps < want) t.warps *= 2;
   t.blocks = (int)((want + t.warps - 1) / t.warps);
-  t.bytes = (((size_t)B + 1) * 8 + 15) / 16 * 16 + (size_t)2 * t.blocks * t.warps * t.row_pad * (D + 1) * 4;
+  t.ok = steps < (1LL << 31);
+  t.bytes = (((size_t)B + 1) * 4 + 15) / 16 * 16 + (size_t)2 * t.blocks * t.warps * t.row_pad * (D + 1) * 4;
   return t;
 }
 
 cudaError_t launch_cache_token(CacheAttendParams p, const TokenSplit& t, void* workspace, cudaStream_t s) {
-  p.prefix = workspace;
-  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + (((size_t)p.B + 1) * 8 + 15) / 16 * 16);
+  p.prefix = static_cast<int*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + (((size_t)p.B + 1) * 4 + 15) / 16 * 16);
   p.part_lse = p.part_o + (size_t)2 * t.blocks * t.warps * t.row_pad * p.D;
   const bool cap = p.softcap > 0.f;
   if (p.D == 64) {

@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "cache_kernels.h"
+#include "ptx.cuh"
 #include "rotary_kernels.h"
 #include "swa_kernels.h"
 
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_backward_kernel(const _
   constexpr int kTok = kRotaryThreads / kPer;
   constexpr int U = 2;
   const int th = threadIdx.x % kPer, row = threadIdx.x / kPer;
+  grid_launch_dependents();
   const int kind = blockIdx.x >= p.blocks[0];
   const int first = kind ? blockIdx.x - p.blocks[0] : blockIdx.x;
   const HeadRows& r = p.grad[kind];
@@ -310,27 +312,28 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_backward_kernel(const _
   }
 }
 
-// dweight[kind][column] = sum of the kind's partial rows: 32 columns and 32 strided runs
-// of rows a block, each run in order, then the runs in order.
+// dweight[kind][column] = sum of the kind's partial rows: a block takes 8 columns, each of
+// its 128 rows of threads a strided run of partials (all its loads in flight at once), and
+// the runs are added up in a tree: one order, whatever the timing.
 __global__ void __launch_bounds__(1024) rotary_weight_kernel(const float* partial, int blocks_q, int blocks_k, int D,
                                                              float* dq_weight, float* dk_weight) {
-  __shared__ double run[32][33];
+  __shared__ double run[128][9];
   const int kind = blockIdx.y;
   float* out = kind ? dk_weight : dq_weight;
   if (!out) return;
-  const int col = blockIdx.x * 32 + threadIdx.x;
+  const int col = blockIdx.x * 8 + threadIdx.x;
   const float* src = partial + (kind ? (long long)blocks_q * D : 0) + col;
   const int n = kind ? blocks_k : blocks_q;
+  grid_dependency_wait();
   double t = 0.0;
-#pragma unroll 4
-  for (int i = threadIdx.y; i < n; i += 32) t += src[(long long)i * D];
+#pragma unroll 8
+  for (int i = threadIdx.y; i < n; i += 128) t += src[(long long)i * D];
   run[threadIdx.y][threadIdx.x] = t;
-  __syncthreads();
-  if (threadIdx.y == 0) {
-    double s = 0.0;
-    for (int i = 0; i < 32; ++i) s += run[i][threadIdx.x];
-    out[col] = (float)s;
+  for (int s = 64; s > 0; s >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.y < s) run[threadIdx.y][threadIdx.x] += run[threadIdx.y + s][threadIdx.x];
   }
+  if (threadIdx.y == 0) out[col] = (float)run[0][threadIdx.x];
 }
 
 __global__ void zero_weight_kernel(float* a, float* b, int n) {
@@ -368,9 +371,17 @@ cudaError_t launch_backward_layout(const RotaryBackwardParams& p, bool norm, boo
   else rotary_backward_kernel<T, G, O, D, false, false><<<grid, kRotaryThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partial) return e;
-  rotary_weight_kernel<<<dim3(D / 32, 2), dim3(32, 32), 0, s>>>(p.partial, p.blocks[0], p.blocks[1], D, p.dweight[0],
-                                                                p.dweight[1]);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(D / 8, 2);
+  cfg.blockDim = dim3(8, 128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rotary_weight_kernel, static_cast<const float*>(p.partial), p.blocks[0], p.blocks[1], D,
+                            p.dweight[0], p.dweight[1]);
 }
 
 template <typename T, typename G, typename O>

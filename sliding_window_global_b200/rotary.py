@@ -5,7 +5,6 @@ kernels, and a call on anything but CUDA tensors raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional
@@ -63,53 +62,62 @@ NO_STRIDES = (0, 0, 0)
 _NO_ROTATION = Rotation(0, 0, None, 1.0)
 _NO_NORM = HeadNorm(0, 0.0, None, None, 0)
 
+# A call of a few microseconds on the GPU is bound by what the host does for it, so the
+# paths below take the cheapest spelling of each step: outputs by empty_like, the stream's
+# handle without a Stream object, and a device or stream context only where it changes
+# something.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-def on_device(t: torch.Tensor, stream):
-    """Context in which a call on ``t`` runs: its device current, and ``stream`` (when
-    given) the one that outputs and workspaces are allocated for."""
+
+def elsewhere(t: torch.Tensor, name: str, stream):
+    """The context a call on ``t`` must enter first (None: it can run as things are): its
+    device current, and ``stream`` the one that outputs and workspaces are allocated for."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if stream is not None:
         if stream.device != t.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
         return torch.cuda.stream(stream)
     if t.get_device() != torch.cuda.current_device():
         return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    return None
 
 
-def current_stream() -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def current_stream(t: torch.Tensor) -> int:
+    return _raw_stream(t.get_device())
 
 
-def check_rows(t: torch.Tensor, name: str, like: torch.Tensor, dims: int, dtype=None):
-    """A tensor of head rows: on the device of ``like``, ``dims`` axes, the last one dense."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+def check_rows(t: torch.Tensor, name: str, device, dims: int, dtype=None):
+    """A tensor of head rows: on ``device``, ``dims`` axes, the last one dense.  Returns its
+    strides."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dim() != dims:
         raise ValueError(f"{name} needs {dims} axes, got {t.dim()}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.stride(-1) != 1 and t.numel() > 0:
+    strides = t.stride()
+    if strides[-1] != 1 and t.numel() > 0:
         raise ValueError(f"the last axis of {name} must be contiguous")
+    return strides
 
 
-def check_index(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape):
+def check_index(t: Optional[torch.Tensor], name: str, device, shape):
     """An int32 tensor of the given shape (or None); returns its address."""
     if t is None:
         return None
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def head_norm(norm_eps, q_weight, k_weight, head_dim: int, like: torch.Tensor) -> HeadNorm:
+def head_norm(norm_eps, q_weight, k_weight, head_dim: int, device) -> HeadNorm:
     """swa_head_norm of the arguments (norm_eps None: no norm)."""
     if norm_eps is None:
         if q_weight is not None or k_weight is not None:
@@ -120,14 +128,14 @@ def head_norm(norm_eps, q_weight, k_weight, head_dim: int, like: torch.Tensor) -
         if w is None:
             ptrs.append(None)
             continue
-        check_rows(w, name, like, 1)
+        check_rows(w, name, device, 1)
         if w.shape[0] != head_dim:
             raise ValueError(f"{name} must have {head_dim} elements, got {w.shape[0]}")
         ptrs.append(w.data_ptr())
         code = _dtype_code(w.dtype)
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise TypeError("q_weight and k_weight must have one dtype")
-    return HeadNorm(1, float(norm_eps), ptrs[0], ptrs[1], code)
+    return HeadNorm(1, norm_eps, ptrs[0], ptrs[1], code)
 
 
 def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -201,36 +209,46 @@ class Rotary:
         ``start + 1``, ... in every batch.  ``norm_eps``: norm every head first, times the
         weights [D].  Outputs are contiguous unless given; an output may be its input.
         Returns ``(q_out, k_out)``."""
-        check_rows(q, "q", q, 4)
+        ctx = elsewhere(q, "q", stream)
+        if ctx is None:
+            return self._forward(q, k, positions, start, norm_eps, q_weight, k_weight, q_out, k_out)
+        with ctx:
+            return self._forward(q, k, positions, start, norm_eps, q_weight, k_weight, q_out, k_out)
+
+    def _forward(self, q, k, positions, start, norm_eps, q_weight, k_weight, q_out, k_out):
+        device, dtype = q.device, q.dtype
+        code = _dtype_code(dtype)
+        qs = check_rows(q, "q", device, 4)
         B, Hq, n, D = q.shape
-        dtype = _dtype_code(q.dtype)
         if D != self.head_dim:
             raise ValueError(f"q has head_dim {D}, expected {self.head_dim}")
-        Hkv = 0
+        Hkv, ks = 0, NO_STRIDES
         if k is not None:
-            check_rows(k, "k", q, 4, q.dtype)
-            Hkv = k.shape[1]
-            if k.shape[0] != B or k.shape[2] != n or k.shape[3] != D:
+            ks = check_rows(k, "k", device, 4, dtype)
+            Bk, Hkv, nk, Dk = k.shape
+            if Bk != B or nk != n or Dk != D:
                 raise ValueError(f"k must be [{B}, heads, {n}, {D}], got {tuple(k.shape)}")
-        with on_device(q, stream):
-            if q_out is None:
-                q_out = torch.empty((B, Hq, n, D), dtype=q.dtype, device=q.device)
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            os = (Hq * n * D, n * D, D)
+        else:
+            os = self._check_out(q_out, "q_out", q)
+        kos, k_ptr, ko_ptr = NO_STRIDES, None, None
+        if k is None:
+            k_out = None
+        else:
+            if k_out is None:
+                k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+                kos = (Hkv * n * D, n * D, D)
             else:
-                self._check_out(q_out, "q_out", q)
-            if k is None:
-                k_out = None
-            elif k_out is None:
-                k_out = torch.empty((B, Hkv, n, D), dtype=q.dtype, device=q.device)
-            else:
-                self._check_out(k_out, "k_out", k)
-            qs, os = q.stride(), q_out.stride()
-            ks, kos = (NO_STRIDES, NO_STRIDES) if k is None else (k.stride(), k_out.stride())
-            a = RotaryArgs(
-                B, n, Hq, Hkv, D, dtype, q.data_ptr(), None if k is None else k.data_ptr(), qs[0], qs[1], qs[2],
-                ks[0], ks[1], ks[2], check_index(positions, "positions", q, (B, n)), int(start), q_out.data_ptr(),
-                None if k is None else k_out.data_ptr(), os[0], os[1], os[2], kos[0], kos[1], kos[2], self.struct,
-                head_norm(norm_eps, q_weight, k_weight, D, q))
-            st = self._lib.swa_rotary_forward(ctypes.byref(a), current_stream())
+                kos = self._check_out(k_out, "k_out", k)
+            k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
+        a = RotaryArgs(
+            B, n, Hq, Hkv, D, code, q.data_ptr(), k_ptr, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
+            check_index(positions, "positions", device, (B, n)), start, q_out.data_ptr(), ko_ptr,
+            os[0], os[1], os[2], kos[0], kos[1], kos[2], self.struct,
+            head_norm(norm_eps, q_weight, k_weight, D, device))
+        st = self._lib.swa_rotary_forward(ctypes.byref(a), current_stream(q))
         if st != 0:
             raise SwaError(st, "swa_rotary_forward")
         return q_out, k_out
@@ -244,68 +262,79 @@ class Rotary:
         bf16).  ``q``, ``k`` are the forward's inputs, required with a norm; they set the
         gradients' dtype and layout (without them, the upstream's).  Returns ``(dq, dk)``, and
         with a norm ``(dq, dk, dq_weight, dk_weight)`` (fp32 [D]; None without that weight)."""
-        check_rows(dq_out, "dq_out", dq_out, 4)
+        ctx = elsewhere(dq_out, "dq_out", stream)
+        if ctx is None:
+            return self._backward(dq_out, dk_out, q, k, positions, start, norm_eps, q_weight, k_weight, dq, dk)
+        with ctx:
+            return self._backward(dq_out, dk_out, q, k, positions, start, norm_eps, q_weight, k_weight, dq, dk)
+
+    def _backward(self, dq_out, dk_out, q, k, positions, start, norm_eps, q_weight, k_weight, dq, dk):
+        device = dq_out.device
+        gs = check_rows(dq_out, "dq_out", device, 4)
         B, Hq, n, D = dq_out.shape
         if D != self.head_dim:
             raise ValueError(f"dq_out has head_dim {D}, expected {self.head_dim}")
-        Hkv = 0
+        Hkv, gks = 0, NO_STRIDES
         if dk_out is not None:
-            check_rows(dk_out, "dk_out", dq_out, 4, dq_out.dtype)
-            Hkv = dk_out.shape[1]
-            if dk_out.shape[0] != B or dk_out.shape[2] != n or dk_out.shape[3] != D:
+            gks = check_rows(dk_out, "dk_out", device, 4, dq_out.dtype)
+            Bk, Hkv, nk, Dk = dk_out.shape
+            if Bk != B or nk != n or Dk != D:
                 raise ValueError(f"dk_out must be [{B}, heads, {n}, {D}], got {tuple(dk_out.shape)}")
         if norm_eps is not None and (q is None or (k is None and Hkv > 0)):
             raise ValueError("the norm's gradient needs q and k")
-        for name, x, g in (("q", q, dq_out), ("k", k, dk_out)):
-            if x is None:
-                continue
-            if g is None:
-                raise ValueError(f"{name} without d{name}_out")
-            check_rows(x, name, dq_out, 4, None if q is None else q.dtype)
-            if x.shape != g.shape:
-                raise ValueError(f"{name} must have shape {tuple(g.shape)}, got {tuple(x.shape)}")
-        with on_device(dq_out, stream):
-            hn = head_norm(norm_eps, q_weight, k_weight, D, dq_out)
-            x_like = q if q is not None else (k if k is not None else dq_out)
-            if dq is None:
-                dq = torch.empty_like(q if q is not None else dq_out, dtype=x_like.dtype)
-            else:
-                self._check_out(dq, "dq", dq_out, dtype=None)
+        qs = ks = NO_STRIDES
+        if q is not None:
+            qs = check_rows(q, "q", device, 4)
+            if q.shape != dq_out.shape:
+                raise ValueError(f"q must have shape {tuple(dq_out.shape)}, got {tuple(q.shape)}")
+        if k is not None:
             if dk_out is None:
-                dk = None
-            elif dk is None:
-                dk = torch.empty_like(k if k is not None else dk_out, dtype=dq.dtype)
+                raise ValueError("k without dk_out")
+            ks = check_rows(k, "k", device, 4, None if q is None else q.dtype)
+            if k.shape != dk_out.shape:
+                raise ValueError(f"k must have shape {tuple(dk_out.shape)}, got {tuple(k.shape)}")
+        hn = head_norm(norm_eps, q_weight, k_weight, D, device)
+        x_dtype = (q if q is not None else k if k is not None else dq_out).dtype
+        if dq is None:
+            dq = torch.empty_like(dq_out, dtype=x_dtype) if q is None else torch.empty_like(q, dtype=x_dtype)
+            os = dq.stride()
+        else:
+            os = self._check_out(dq, "dq", dq_out, None)
+        oks, gk_ptr, dk_ptr = NO_STRIDES, None, None
+        if dk_out is None:
+            dk = None
+        else:
+            if dk is None:
+                dk = torch.empty_like(dk_out if k is None else k, dtype=dq.dtype)
+                oks = dk.stride()
             else:
-                self._check_out(dk, "dk", dk_out, dtype=dq.dtype)
-            dqw = dkw = None
-            if q_weight is not None:
-                dqw = torch.empty(D, dtype=torch.float32, device=dq_out.device)
-            if k_weight is not None and Hkv > 0:
-                dkw = torch.empty(D, dtype=torch.float32, device=dq_out.device)
-            has_k = dk_out is not None
-            qs = NO_STRIDES if q is None else q.stride()
-            ks = NO_STRIDES if k is None else k.stride()
-            gs, os = dq_out.stride(), dq.stride()
-            gks, oks = (dk_out.stride(), dk.stride()) if has_k else (NO_STRIDES, NO_STRIDES)
-            a = RotaryBackwardArgs(
-                B, n, Hq, Hkv, D, _dtype_code(x_like.dtype), _dtype_code(dq_out.dtype), _dtype_code(dq.dtype),
-                None if q is None else q.data_ptr(), None if k is None else k.data_ptr(), qs[0], qs[1], qs[2],
-                ks[0], ks[1], ks[2], check_index(positions, "positions", dq_out, (B, n)), int(start),
-                dq_out.data_ptr(), dk_out.data_ptr() if has_k else None, gs[0], gs[1], gs[2], gks[0], gks[1], gks[2],
-                dq.data_ptr(), dk.data_ptr() if has_k else None, os[0], os[1], os[2], oks[0], oks[1], oks[2],
-                None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(), self.struct, hn,
-                None, 0)
-            if dqw is not None or dkw is not None:
-                need = self._lib.swa_rotary_workspace_bytes(ctypes.byref(a))
-                ws = torch.empty(need, dtype=torch.uint8, device=dq_out.device)
-                a.workspace, a.workspace_bytes = ws.data_ptr(), need
-            st = self._lib.swa_rotary_backward(ctypes.byref(a), current_stream())
+                oks = self._check_out(dk, "dk", dk_out, dq.dtype)
+            gk_ptr, dk_ptr = dk_out.data_ptr(), dk.data_ptr()
+        dqw = dkw = None
+        if q_weight is not None:
+            dqw = torch.empty_like(q_weight, dtype=torch.float32)
+        if k_weight is not None and Hkv > 0:
+            dkw = torch.empty_like(k_weight, dtype=torch.float32)
+        a = RotaryBackwardArgs(
+            B, n, Hq, Hkv, D, _dtype_code(x_dtype), _dtype_code(dq_out.dtype), _dtype_code(dq.dtype),
+            None if q is None else q.data_ptr(), None if k is None else k.data_ptr(), qs[0], qs[1], qs[2],
+            ks[0], ks[1], ks[2], check_index(positions, "positions", device, (B, n)), start, dq_out.data_ptr(), gk_ptr,
+            gs[0], gs[1], gs[2], gks[0], gks[1], gks[2], dq.data_ptr(), dk_ptr, os[0], os[1], os[2], oks[0], oks[1],
+            oks[2], None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(), self.struct, hn,
+            None, 0)
+        ref = ctypes.byref(a)
+        if dqw is not None or dkw is not None:
+            need = self._lib.swa_rotary_workspace_bytes(ref)
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            a.workspace, a.workspace_bytes = ws.data_ptr(), need
+        st = self._lib.swa_rotary_backward(ref, current_stream(dq_out))
         if st != 0:
             raise SwaError(st, "swa_rotary_backward")
         return (dq, dk) if norm_eps is None else (dq, dk, dqw, dkw)
 
     @staticmethod
     def _check_out(t, name, like, dtype=0):
-        check_rows(t, name, like, like.dim(), like.dtype if dtype == 0 else dtype)
+        strides = check_rows(t, name, like.device, 4, like.dtype if dtype == 0 else dtype)
         if t.shape != like.shape:
             raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+        return strides
