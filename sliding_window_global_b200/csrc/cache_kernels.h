@@ -55,6 +55,7 @@ struct CacheAttendParams {
 // how its warps are laid out, from sizes only.
 constexpr int kTokenRows = 32;
 struct TokenSplit {
+  int cluster;                      // blocks that share a unit; 0: runs of equal length instead
   int warps, blocks;                // warps of a block, blocks
   int row_pad;                      // rows of a partial result
   bool ok;                          // the steps can be counted in 31 bits

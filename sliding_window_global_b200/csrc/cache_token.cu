@@ -12,6 +12,11 @@
 // 128-row tcgen05 products would only compute padding).  A unit that lies in one warp's run
 // is stored directly; one that is split leaves a partial result a warp, which the merge
 // kernel joins in the order of the keys.
+//
+// Where the keys in reach are few, the second launch and the search for a warp's run cost
+// more than uneven work does: then a unit belongs to a cluster of one to eight blocks, its
+// steps are shared out among their warps, and the parts are joined through shared memory of
+// the block and of the cluster (UNIT; the rule stands at token_split).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -121,33 +126,155 @@ struct Runs {
   }
 };
 
-template <int D, int MT, bool CAP>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __grid_constant__ CacheAttendParams p) {
+// Shared memory of another block of the cluster.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+  uint32_t at;
+  float x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ float2 ld_cluster2(const float* p, uint32_t rank) {
+  uint32_t at;
+  float2 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// UNIT: joins the warps' parts of a unit, first those of a block, then the blocks', both in
+// the order of the keys, and writes the unit's rows.  Every thread of the cluster calls it.
+// The rings are free: each warp has computed what it fetched.
+template <int D, int MT>
+__device__ __forceinline__ void join_unit(const CacheAttendParams& p, const CacheSeq& s, int hk, int rows, int cluster,
+                                          uint8_t* smem, float (&o)[MT][D / 8][4], float (&m)[MT][2],
+                                          float (&l)[MT][2]) {
+  constexpr int R = 16 * MT, LD = D + 8;               // rows 32 bytes apart in the banks
+  __shared__ float sM[kMaxWarps][R], sL[kMaxWarps][R], sTop[R], sSum[R];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, wb = blockDim.x >> 5;
+  float* parts = reinterpret_cast<float*>(smem);       // [warps][R][LD]
+  cp_async_wait<0>();
+  __syncthreads();
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float sum = l[mt][x];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int r = mt * 16 + (lane >> 2) + 8 * x;
+      if (r >= rows) continue;
+      float2* part = reinterpret_cast<float2*>(parts + (wid * R + r) * LD + 2 * (lane & 3));
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) part[4 * e] = make_float2(o[mt][e][2 * x], o[mt][e][2 * x + 1]);
+      if ((lane & 3) == 0) {
+        sM[wid][r] = m[mt][x];
+        sL[wid][r] = sum;
+      }
+    }
+  }
+  __syncthreads();
+  const int pairs = rows * (D / 2);
+  auto store = [&](int i, float2 acc, float top, float sum) {
+    const int r = i / (D / 2), c = i % (D / 2) * 2;
+    const bool has = top != -INFINITY;
+    const float inv = has ? 1.f / sum : 0.f;
+    const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + row * D + c) = pack_bf16x2(acc.x * inv, acc.y * inv);
+    if (p.lse && c == 0) p.lse[row] = has ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  };
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+    const int r = i / (D / 2), c = i % (D / 2) * 2;
+    float top = -INFINITY, sum = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+    for (int k = 0; k < wb; ++k) top = fmaxf(top, sM[k][r]);
+    for (int k = 0; k < wb; ++k) {
+      if (sM[k][r] == -INFINITY) continue;             // no key in this part (a NaN sum goes on)
+      const float f = ex2_approx(sM[k][r] - top);
+      const float2 x = *reinterpret_cast<const float2*>(parts + (k * R + r) * LD + c);
+      sum += f * sL[k][r];
+      acc.x += f * x.x;
+      acc.y += f * x.y;
+    }
+    if (cluster == 1) {
+      store(i, acc, top, sum);
+    } else {
+      *reinterpret_cast<float2*>(parts + r * LD + c) = acc;      // over warp 0's part: read by this thread alone
+      if (c == 0) {
+        sTop[r] = top;
+        sSum[r] = sum;
+      }
+    }
+  }
+  if (cluster == 1) return;
+  cluster_sync();
+  for (int i = cluster_rank() * blockDim.x + threadIdx.x; i < pairs; i += cluster * blockDim.x) {
+    const int r = i / (D / 2), c = i % (D / 2) * 2;
+    float top = -INFINITY, sum = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+    for (int k = 0; k < cluster; ++k) top = fmaxf(top, ld_cluster(&sTop[r], k));
+    for (int k = 0; k < cluster; ++k) {
+      const float t = ld_cluster(&sTop[r], k);
+      if (t == -INFINITY) continue;
+      const float f = ex2_approx(t - top);
+      const float2 x = ld_cluster2(parts + r * LD + c, k);
+      sum += f * ld_cluster(&sSum[r], k);
+      acc.x += f * x.x;
+      acc.y += f * x.y;
+    }
+    store(i, acc, top, sum);
+  }
+  cluster_sync();                                      // nobody leaves while its memory is read
+}
+
+template <int D, int MT, bool CAP, bool UNIT>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __grid_constant__ CacheAttendParams p,
+                                                                         int cluster) {
   using S = Step<D>;
   constexpr int NG = S::kGroups;
   constexpr int CH = D / 8;                            // 16-byte chunks of a row
   extern __shared__ __align__(128) uint8_t smem[];
-  const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), W = gridDim.x * (blockDim.x >> 5);
-  const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * kStages * S::kBytes;
-  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, wb = blockDim.x >> 5;
+  const int w = blockIdx.x * wb + wid, W = gridDim.x * wb;
+  const uint32_t ring = smem_u32(smem) + wid * kStages * S::kBytes;
 
   // ---- this warp's run, and the sequence, head and step it starts at
-  int last_first = 0, last_mine = 0;       // of the last 32 sequences: with B <= 32, of all
-  const int n = scan_steps<D>(p, lane, [&](int b, int first, int mine, bool bad) {
-    last_first = first;
-    last_mine = mine;
-    if (w != 0 || b >= p.B) return;
-    p.prefix[b] = first;
-    if (bad) atomicOr(p.err, kDevErrCheck);
-  });
-  if (w == 0 && lane == 0) p.prefix[p.B] = n;
-  const Runs runs(n, W);
-  const int begin = runs.begin(w);
-  const int total = runs.begin(w + 1) - begin;
-  if (total == 0) return;
-  int b = 0, hk = 0, j = 0;
-  {
+  int b = 0, hk = 0, j = 0, total = 0;
+  TokenUnit unit = {};                                 // UNIT: the cluster's
+  if (UNIT) {
+    const int id = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    b = id / p.Hkv;
+    hk = id % p.Hkv;
+    unit = token_unit<D>(p, b);
+    if (unit.s.bad && hk == 0 && rank == 0 && threadIdx.x == 0) atomicOr(p.err, kDevErrCheck);
+    if (unit.steps == 0) return;                       // no new tokens: the whole cluster leaves
+    const Runs runs(unit.steps, cluster * wb);
+    j = runs.begin(rank * wb + wid);
+    total = runs.begin(rank * wb + wid + 1) - j;
+  } else {
+    grid_launch_dependents();
+    int last_first = 0, last_mine = 0;       // of the last 32 sequences: with B <= 32, of all
+    const int n = scan_steps<D>(p, lane, [&](int bb, int first, int mine, bool bad) {
+      last_first = first;
+      last_mine = mine;
+      if (w != 0 || bb >= p.B) return;
+      p.prefix[bb] = first;
+      if (bad) atomicOr(p.err, kDevErrCheck);
+    });
+    if (w == 0 && lane == 0) p.prefix[p.B] = n;
+    const Runs runs(n, W);
+    const int begin = runs.begin(w);
+    total = runs.begin(w + 1) - begin;
+    if (total == 0) return;
     int first = 0, steps = 1;
     auto look = [&](int bb, int ff, int mine, bool) {
       const unsigned hit = __ballot_sync(0xffffffffu, ff <= begin && begin < ff + mine);
@@ -165,7 +292,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
   }
 
   // ---- fetching side: its own place in the list, kStages - 1 steps ahead
-  TokenUnit fu = token_unit<D>(p, b);
+  TokenUnit fu = UNIT ? unit : token_unit<D>(p, b);
   int fb = b, fhk = hk, fj = j;
   int fpage[NG];
   unsigned history = 0;                    // per group of a fetched step: its page exists (newest lowest)
@@ -176,7 +303,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
       fpage[g] = key < fu.hi ? __ldg(p.block_table + (long long)fb * p.max_pages + key / p.page_size) : 0;
     }
   };
-  look_up();
+  if (total > 0) look_up();
   int fetched = 0;
   auto fetch = [&]() {
     if (fetched < total) {
@@ -201,7 +328,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
         }
       }
       ++fetched;
-      if (++fj == fu.steps) {
+      if (++fj == fu.steps && !UNIT) {
         fj = 0;
         if (++fhk == p.Hkv) {
           fhk = 0;
@@ -224,8 +351,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
   const float cap_l2 = p.softcap * kLog2e;             // CAP: cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
   const float cap_in = CAP ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
   int done = 0;
-  while (done < total) {
-    const TokenUnit u = token_unit<D>(p, b);
+  while (UNIT || done < total) {
+    const TokenUnit u = UNIT ? unit : token_unit<D>(p, b);
     const int rows = u.s.count * p.G;
     uint32_t qf[MT][D / 16][4];
     int klo[MT][2], khi[MT][2];
@@ -264,7 +391,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
         for (int c = 0; c < 4; ++c) o[mt][e][c] = 0.f;
     }
     const bool from_start = j == 0;
-    while (true) {
+    while (done < total) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
       fetch();                             // into the slot of the step before, which every lane has read
@@ -362,7 +489,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
       }
       ++done;
       ++j;
-      if (j == u.steps || done == total) break;
+      if (j == u.steps) break;
+    }
+
+    if (UNIT) {
+      join_unit<D, MT>(p, u.s, hk, rows, cluster, smem, o, m, l);
+      return;
     }
 
     // ---- the unit (or this run's part of it) is done
@@ -474,36 +606,70 @@ __global__ void __launch_bounds__(128) cache_token_merge_kernel(const __grid_con
 
 template <int D, int MT, bool CAP>
 cudaError_t launch_token(const CacheAttendParams& p, const TokenSplit& t, cudaStream_t s) {
-  cudaError_t e = allow_smem<&cache_token_kernel<D, MT, CAP>>(kMaxWarps * kStages * Step<D>::kBytes);
-  if (e != cudaSuccess) return e;
-  cache_token_kernel<D, MT, CAP><<<t.blocks, t.warps * 32, t.warps * kStages * Step<D>::kBytes, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  const int smem = t.warps * kStages * Step<D>::kBytes;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.max_tokens * p.G));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (t.cluster) {
+    cudaError_t e = allow_smem<&cache_token_kernel<D, MT, CAP, true>>(kMaxWarps * kStages * Step<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = t.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(t.blocks);
+    cfg.blockDim = dim3(t.warps * 32);
+    cfg.dynamicSmemBytes = smem;
+    return cudaLaunchKernelEx(&cfg, cache_token_kernel<D, MT, CAP, true>, p, t.cluster);
+  }
+  cudaError_t e = allow_smem<&cache_token_kernel<D, MT, CAP, false>>(kMaxWarps * kStages * Step<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  cache_token_kernel<D, MT, CAP, false><<<t.blocks, t.warps * 32, smem, s>>>(p, 0);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.max_tokens * p.G));
+  cfg.blockDim = dim3(128);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, cache_token_merge_kernel<D>, p, t.blocks * t.warps, 16 * MT);
 }
+
+// Shared memory of the joined parts fits into the rings they replace.
+static_assert(32 * (128 + 8) * 4 <= kStages * Step<128>::kBytes && 32 * (64 + 8) * 4 <= kStages * Step<64>::kBytes,
+              "parts of a warp");
 
 }  // namespace
 
 TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach) {
-  TokenSplit t;
+  TokenSplit t = {};
   t.row_pad = rows <= 16 ? 16 : 32;
   const int keys = 2048 / D;
-  const long long steps = (long long)B * Hkv * ((reach + keys - 1) / keys + 1);
+  const long long unit_steps = (reach + keys - 1) / keys + 1, units = (long long)B * Hkv;
+  const long long steps = units * unit_steps;
+  t.ok = steps < (1LL << 31);
+  // A cluster for each unit, as many blocks as the GPU holds at once, two steps a warp at
+  // least; with more units than SMs, blocks of four warps, two of them on an SM.
+  int cluster = 1, warps = units > 148 ? 4 : kMaxWarps;
+  while (cluster < 8 && units * cluster * 2 <= 148 && unit_steps > cluster * warps * 2) cluster *= 2;
+  while (warps > 1 && unit_steps <= warps) warps /= 2;
+  const long long slots = 148 * (kMaxWarps / warps);
+  const long long waves = (units * cluster + slots - 1) / slots;
+  const long long per_unit = waves * ((unit_steps + cluster * warps - 1) / (cluster * warps));
+  // Equal runs of all steps: better balanced, but a launch and a search more (about six
+  // steps' time).
+  const long long per_run = (steps + 148 * kMaxWarps - 1) / (148 * kMaxWarps);
+  if (per_unit <= per_run + 6 && units * cluster < (1LL << 31)) {
+    t.cluster = cluster;
+    t.warps = warps;
+    t.blocks = (int)(units * cluster);
+    return t;
+  }
   // Two steps a warp at least; one block an SM, of as few warps as that allows.
   const long long want = std::min<long long>((steps + 1) / 2, 148 * kMaxWarps);
   t.warps = 1;
   while (t.warps < kMaxWarps && 148 * t.warps < want) t.warps *= 2;
   t.blocks = (int)((want + t.warps - 1) / t.warps);
-  t.ok = steps < (1LL << 31);
   t.bytes = (((size_t)B + 1) * 4 + 15) / 16 * 16 + (size_t)2 * t.blocks * t.warps * t.row_pad * (D + 1) * 4;
   return t;
 }

@@ -300,6 +300,9 @@ ATTENDS = [
     ("tokens_cap", BF16, 16, 2, 128, 16, None, 5.0, [1] * 3, [33, 300, 1]),
     ("long_split", BF16, 8, 1, 64, 128, None, 0.0, [1], [9001]),
     ("long_split_cap", BF16, 3, 1, 128, 32, 6000, 30.0, [1, 1], [7001, 40]),
+    ("many_short", BF16, 8, 4, 64, 16, None, 0.0, [1] * 50, [1 + 37 * i % 211 for i in range(50)]),
+    ("many_uneven", BF16, 4, 1, 128, 64, None, 30.0, [1] * 40, [1 + 977 * i % 2999 for i in range(39)] + [12000]),
+    ("cluster", BF16, 6, 1, 128, 16, 900, 0.0, [2, 1], [700, 2000]),
     ("guesses", BF16, 10, 2, 128, 16, None, 0.0, [3] * 3, [3, 50, 517]),
     ("guesses_window", BF16, 40, 8, 64, 16, 17, 0.0, [8, 1, 5, 0], [8, 20, 300, 77]),
     ("wide_group", BF16, 24, 1, 64, 32, None, 0.0, [1, 2], [100, 400]),
