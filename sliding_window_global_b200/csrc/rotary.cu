@@ -6,7 +6,7 @@
 // What bounds it: every element is read once and written once for a handful of
 // operations, so memory does.  A block takes 16 (D = 128) or 32 (D = 64) tokens and a
 // run of heads; a thread keeps the cosines and sines of its eight pairs in registers
-// for all those heads (they depend on the token only), and loads kUnroll heads ahead of
+// for all those heads (they depend on the token only), and loads a group of heads ahead of
 // the arithmetic, which keeps enough bytes in flight.  Rows may lie anywhere: a
 // projection's token-major output is read in place and written head-major, in runs of
 // 16 bytes a thread and 128 or more a row.
@@ -23,10 +23,18 @@ namespace swa {
 namespace {
 
 constexpr int kRotaryThreads = 128;
+// Heads of a block at most. Forward, a 2 x 8191-token normed prompt: 57.5 us with 32, 59.7 with
+// 16. Backward, a normed 16384-token prompt: 131 us with 16, whose items the blocks share
+// out evenly, 134 with 8, 143 with 32.
+constexpr int kForwardRun = 32, kBackwardRun = 16;
+// Blocks of an SM that the registers must allow. Forward: four (128 registers; 104.5 us for
+// the plain 32768-token prompt, 106.7 without the bound). Backward: five without a norm; with
+// one the compiler's own choice of 168 registers, since four blocks would spill (131 to 163 us).
+constexpr int kForwardBlocks = 4, kBackwardBlocks = 5;
 
 template <typename T>
 __host__ __device__ constexpr int unroll_heads() {
-  return sizeof(T) == 2 ? 4 : 2;
+  return sizeof(T) == 2 ? 4 : 1;
 }
 
 // Which kind of rows block `y` works on, and which run of its heads.
@@ -97,7 +105,7 @@ __device__ __forceinline__ CacheToken cache_token(const RotaryParams& p, int tok
 }
 
 template <typename T, int D, bool NORM, bool INTER, bool CACHE>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kRotaryThreads, kForwardBlocks) rotary_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int kPer = D / 16;                             // threads of a row
   constexpr int U = unroll_heads<T>();
   const int th = threadIdx.x % kPer;
@@ -105,50 +113,61 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
   const Segment sg = segment_of(p.segs, CACHE ? 3 : 2, blockIdx.y);
   const HeadRows& r = p.rows[sg.kind];
   const int h_begin = sg.run * p.heads_per_seg, h_end = min(r.heads, h_begin + p.heads_per_seg);
-  bool ok = tok < p.tokens;
+  const bool live = tok < p.tokens;
+  const int batch = live && !CACHE ? (int)tok / p.n : 0, at = live && !CACHE ? (int)tok % p.n : 0;
+  const ChunkPair cp = chunk_pair<D, INTER>(th, p.m.rot);
+  const T* src = static_cast<const T*>(r.src) + (CACHE ? tok * r.st : batch * r.sb + at * r.st);
+  // The loads run one group of heads ahead of the arithmetic, the first one ahead of the
+  // token's place and its cosines.
+  Chunk<T> na[U], nb[U];
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      na[u] = Chunk<T>{};
+      nb[u] = Chunk<T>{};
+      if (live && h0 + u < h_end) {
+        const T* x = src + (h0 + u) * r.sh;
+        na[u] = load_chunk(x + 8 * cp.a);
+        nb[u] = load_chunk(x + 8 * cp.b);
+      }
+    }
+  };
+  fetch(h_begin);
+  bool ok = live;
   int pos = 0;
-  long long src_off = 0, dst_off = 0, dst_head = r.dh;
+  long long dst_off = 0, dst_head = r.dh;
   if (CACHE) {
     const CacheToken t = cache_token(p, (int)min(tok, (long long)p.tokens));
     ok = t.ok;
     pos = t.pos;
-    src_off = tok * r.st;
     if (sg.kind == 0) {
       dst_off = tok * r.dt;
     } else {
       dst_off = t.page_row * D;
       dst_head = (long long)p.page_size * D;
     }
-  } else if (ok) {
-    const int b = (int)tok / p.n, i = (int)tok % p.n;
-    pos = p.positions ? __ldg(p.positions + tok) : (int)((unsigned)p.start + (unsigned)i);
-    src_off = b * r.sb + i * r.st;
-    dst_off = b * r.db + i * r.dt;
+  } else if (live) {
+    pos = p.positions ? __ldg(p.positions + tok) : (int)((unsigned)p.start + (unsigned)at);
+    dst_off = batch * r.db + at * r.dt;
   }
-  const ChunkPair cp = chunk_pair<D, INTER>(th, p.m.rot);
-  const T* src = static_cast<const T*>(r.src) + src_off;
   T* dst = static_cast<T*>(r.dst) + dst_off;
   const bool copy = CACHE && sg.kind == 2;                 // values are stored as they come
   float cs[8], sn[8], wa[8], wb[8];
   if (!copy) {
-    rotary_table<D, INTER>(p.m, cp, pos, cs, sn);
     if (NORM) {
       load_weights(r.weight, p.m.weight_bf16, cp.a, wa);
       load_weights(r.weight, p.m.weight_bf16, cp.b, wb);
     }
+    rotary_table<D, INTER>(p.m, cp, pos, cs, sn);
   }
   for (int h0 = h_begin; h0 < h_end; h0 += U) {
     Chunk<T> a[U], b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      a[u] = Chunk<T>{};
-      b[u] = Chunk<T>{};
-      if (ok && h0 + u < h_end) {
-        const T* x = src + (h0 + u) * r.sh;
-        a[u] = load_chunk(x + 8 * cp.a);
-        b[u] = load_chunk(x + 8 * cp.b);
-      }
+      a[u] = na[u];
+      b[u] = nb[u];
     }
+    fetch(h0 + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!copy) {
@@ -184,11 +203,11 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
 // Each block adds up its rows' dw in registers and writes one partial row; the
 // reduction below adds the partials in a fixed order.
 template <typename T, typename G, typename O, int D, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_backward_kernel(const __grid_constant__
+__global__ void __launch_bounds__(kRotaryThreads, NORM ? 1 : kBackwardBlocks) rotary_backward_kernel(const __grid_constant__
                                                                              RotaryBackwardParams p) {
   constexpr int kPer = D / 16;
   constexpr int kTok = kRotaryThreads / kPer;
-  constexpr int U = 2;
+  constexpr int U = 1;
   const int th = threadIdx.x % kPer, row = threadIdx.x / kPer;
   grid_launch_dependents();
   const int kind = blockIdx.x >= p.blocks[0];
@@ -221,6 +240,26 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_backward_kernel(const _
     const G* g = static_cast<const G*>(r.src) + g_off;
     O* o = static_cast<O*>(r.dst) + o_off;
     const T* x = static_cast<const T*>(p.x[kind]) + x_off;
+    Chunk<G> nga[U], ngb[U];
+    Chunk<T> nxa[U], nxb[U];
+    auto fetch = [&](int h0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        nga[u] = ngb[u] = Chunk<G>{};
+        nxa[u] = nxb[u] = Chunk<T>{};
+        if (ok && h0 + u < he) {
+          const G* gp = g + (h0 + u) * r.sh;
+          nga[u] = load_chunk(gp + 8 * cp.a);
+          ngb[u] = load_chunk(gp + 8 * cp.b);
+          if (NORM) {
+            const T* xp = x + (h0 + u) * p.xh[kind];
+            nxa[u] = load_chunk(xp + 8 * cp.a);
+            nxb[u] = load_chunk(xp + 8 * cp.b);
+          }
+        }
+      }
+    };
+    fetch(hs);                             // as in the forward kernel, ahead of the arithmetic
     float cs[8], sn[8];
     rotary_table<D, INTER>(p.m, cp, pos, cs, sn);
     for (int h0 = hs; h0 < he; h0 += U) {
@@ -228,19 +267,12 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_backward_kernel(const _
       Chunk<T> xa[U], xb[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        ga[u] = gb[u] = Chunk<G>{};
-        xa[u] = xb[u] = Chunk<T>{};
-        if (ok && h0 + u < he) {
-          const G* gp = g + (h0 + u) * r.sh;
-          ga[u] = load_chunk(gp + 8 * cp.a);
-          gb[u] = load_chunk(gp + 8 * cp.b);
-          if (NORM) {
-            const T* xp = x + (h0 + u) * p.xh[kind];
-            xa[u] = load_chunk(xp + 8 * cp.a);
-            xb[u] = load_chunk(xp + 8 * cp.b);
-          }
-        }
+        ga[u] = nga[u];
+        gb[u] = ngb[u];
+        xa[u] = nxa[u];
+        xb[u] = nxb[u];
       }
+      fetch(h0 + U);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float ha[8], hb[8];
@@ -446,12 +478,12 @@ swa_status make_rotary_math(const swa_rotation& r, const swa_head_norm& n, int D
   return SWA_OK;
 }
 
-int split_heads(long long token_tiles, const int* heads, int kinds, int* segs) {
+int split_heads(long long token_tiles, const int* heads, int kinds, int longest, int* segs) {
   // Longer runs of heads reuse a token's cosines; shorter ones make more blocks.  Halve
   // the runs until the call has eight blocks an SM.
   int per = 1;
   for (int i = 0; i < kinds; ++i)
-    while (per < heads[i] && per < 16) per *= 2;
+    while (per < heads[i] && per < longest) per *= 2;
   while (true) {
     long long blocks = 0;
     for (int i = 0; i < kinds; ++i) {
@@ -500,7 +532,7 @@ swa_status swa_rotary_forward(const swa_rotary_args* a, void* stream) {
   p.start = a->start;
   const int heads[2] = {a->num_q_heads, Hk};
   const int tile = swa::rotary_tile_tokens(D);
-  p.heads_per_seg = swa::split_heads((tokens + tile - 1) / tile, heads, 2, p.segs);
+  p.heads_per_seg = swa::split_heads((tokens + tile - 1) / tile, heads, 2, swa::kForwardRun, p.segs);
   if (p.segs[0] + p.segs[1] > 65535) return SWA_ERR_UNSUPPORTED;
   const bool norm = a->head_norm.norm, inter = a->rotation.interleaved;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -513,21 +545,24 @@ swa_status swa_rotary_forward(const swa_rotary_args* a, void* stream) {
 namespace swa {
 namespace {
 
-constexpr int kMaxBackwardBlocks = 148 * 6;
+constexpr long long kMaxNormBlocks = 148 * 6;
 
-// Blocks of the backward kernel: one an item (tile of tokens, run of heads) up to six an
-// SM, shared between q and k by their heads.  Depends on sizes only.
+// Blocks of the backward kernel: one an item (tile of tokens, run of heads); with a norm, whose
+// weights' partial sums each block leaves, six an SM at most, shared between q and k by their
+// heads.  Depends on sizes only.
 void backward_split(const swa_rotary_backward_args& a, int* segs, int* blocks, int* per) {
   const int tile = rotary_tile_tokens(a.head_dim);
   const long long tiles = ((long long)a.batch * a.seq_len + tile - 1) / tile;
   const int heads[2] = {a.num_q_heads, a.num_kv_heads};
-  *per = split_heads(tiles, heads, 2, segs);
+  *per = split_heads(tiles, heads, 2, kBackwardRun, segs);
   const long long items[2] = {tiles * segs[0], tiles * segs[1]};
-  const long long all = items[0] + items[1], cap = std::min<long long>(all, kMaxBackwardBlocks);
-  blocks[1] = items[1] == 0 ? 0
-                            : (int)std::min<long long>(items[1], std::max<long long>(
-                                                                     1, cap * heads[1] / (heads[0] + heads[1])));
-  blocks[0] = (int)std::min<long long>(items[0], std::max<long long>(1, cap - blocks[1]));
+  const long long all = items[0] + items[1], cap = std::min<long long>(all, a.head_norm.norm ? kMaxNormBlocks : 1LL << 30);
+  // shares in proportion to the heads, then as few blocks as keep the longest block's items
+  const long long share[2] = {cap * heads[0] / (heads[0] + heads[1]), cap * heads[1] / (heads[0] + heads[1])};
+  for (int i = 0; i < 2; ++i) {
+    const long long rounds = (items[i] + std::max<long long>(share[i], 1) - 1) / std::max<long long>(share[i], 1);
+    blocks[i] = rounds == 0 ? 0 : (int)((items[i] + rounds - 1) / rounds);
+  }
 }
 
 bool backward_sizes_ok(const swa_rotary_backward_args& a) {
@@ -653,7 +688,7 @@ swa_status swa_cache_append(const swa_cache* cache, const swa_cache_batch* batch
   p.err = cache->error_word;
   const int heads[3] = {Hq, Hk, Hk};
   const int tile = swa::rotary_tile_tokens(D);
-  p.heads_per_seg = swa::split_heads((T + tile - 1) / tile, heads, 3, p.segs);
+  p.heads_per_seg = swa::split_heads((T + tile - 1) / tile, heads, 3, swa::kForwardRun, p.segs);
   if (p.segs[0] + p.segs[1] + p.segs[2] > 65535) return SWA_ERR_UNSUPPORTED;
   const bool norm = a->head_norm.norm, inter = a->rotation.interleaved;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

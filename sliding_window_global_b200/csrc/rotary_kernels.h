@@ -55,9 +55,9 @@ struct RotaryBackwardParams {
 // Check a rotation and a head norm for heads of D elements and fill in *m.
 swa_status make_rotary_math(const swa_rotation& r, const swa_head_norm& n, int D, RotaryMath* m);
 
-// Heads per block so that a call of few tokens still spreads over the GPU, and the
-// resulting blocks along each kind's heads.
-int split_heads(long long token_tiles, const int* heads, int kinds, int* segs);
+// Heads per block, `longest` at most, so that a call of few tokens still spreads over the
+// GPU, and the resulting blocks along each kind's heads.
+int split_heads(long long token_tiles, const int* heads, int kinds, int longest, int* segs);
 
 // Tokens of one block.
 int rotary_tile_tokens(int D);
