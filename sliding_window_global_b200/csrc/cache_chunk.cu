@@ -578,24 +578,20 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         }
         const int key0 = pc.en.base + j * kTile;
         const int lo_t = klo - key0, hi_t = khi - key0;
-        uint32_t live = 0;                 // 32-column chunks with a key for any row of the warp
+        uint32_t live = 0xF;               // 32-column chunks with a key for any row of the warp
+        if (key0 < all_lo || key0 + kTile > all_hi || miss) {
+          // One path for every kind of mask (a bit a key): the loop has to stay small, since
+          // its instructions are fetched anew on every way around.
+          live = 0;
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
-          if (__any_sync(0xffffffffu, lo_t < 32 * ch + 32 && hi_t > 32 * ch)) live |= 1u << ch;
-        const bool cut_lo = key0 < all_lo, cut_hi = key0 + kTile > all_hi;
-        if (cut_lo && cut_hi) {
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t keep = lo_t <= 32 * ch ? ~0u : lo_t >= 32 * ch + 32 ? 0u : ~0u << (lo_t - 32 * ch);
+            keep &= hi_t >= 32 * ch + 32 ? ~0u : hi_t <= 32 * ch ? 0u : ~(~0u << (hi_t - 32 * ch));
+            keep &= ((miss >> (2 * ch)) & 1 ? 0u : 0xffffu) | ((miss >> (2 * ch + 1)) & 1 ? 0u : 0xffff0000u);
+            if (__any_sync(0xffffffffu, keep != 0)) live |= 1u << ch;
 #pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = (e >= lo_t && e < hi_t) ? s[e] : -INFINITY;
-        } else if (cut_lo) {
-#pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = (e >= lo_t) ? s[e] : -INFINITY;
-        } else if (cut_hi) {
-#pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = (e < hi_t) ? s[e] : -INFINITY;
-        }
-        if (miss) {
-#pragma unroll
-          for (int e = 0; e < kTile; ++e) s[e] = (miss >> (e / 16) & 1) ? -INFINITY : s[e];
+            for (int e = 0; e < 32; ++e) s[32 * ch + e] = (keep >> e & 1) ? s[32 * ch + e] : -INFINITY;
+          }
         }
         const float mul = CAP ? 1.f : sl2;
         const float m_new = fmaxf(m, row_max(s) * mul);
@@ -675,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       const int rows_here = min(h.tokens * p.a.G - (warp & 3) * 32, 32);       // rows of this warp that exist
       uint8_t* stage = smem + C::kOutOff + warp * 4096;
       const int sw_row = lane >> 3, sw_chunk = lane & 7;
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < (whole ? D / 64 : D / 32); ++half) {
         if (whole) {
 #pragma unroll
