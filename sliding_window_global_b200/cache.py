@@ -45,6 +45,9 @@ class CacheAttendArgs(ctypes.Structure):
     ]
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
 class PagedCache:
     """Keys and values of many sequences in pages of ``page_size`` positions:
     ``k_pages`` and ``v_pages`` are contiguous [num_pages, Hkv, page_size, D] (bf16 or fp32,
@@ -166,6 +169,10 @@ class PagedCache:
             window = -1
         elif window < 0:
             raise ValueError("window must be None or at least 0")
+        # bounds beyond what an int32 length can reach bound nothing
+        window = min(window, _INT_MAX)
+        max_len = min(max_len, _INT_MAX)
+        max_tokens = T if max_tokens is None else min(max_tokens, T)
         batch = self._batch(T, seq_lens, block_table, cu_tokens)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -179,7 +186,7 @@ class PagedCache:
         elif lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous() or \
                 lse.device != self._device:
             raise ValueError(f"lse must be a contiguous fp32 [{T}, {Hq}] on {self._device}")
-        a = CacheAttendArgs(Hq, q.data_ptr(), qs[0], qs[1], T if max_tokens is None else max_tokens, max_len, window,
+        a = CacheAttendArgs(Hq, q.data_ptr(), qs[0], qs[1], max_tokens, max_len, window,
                             softcap, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), None, 0)
         refs = self._ref, ctypes.byref(batch), ctypes.byref(a)
         need = self._lib.swa_cache_attend_workspace_bytes(*refs)

@@ -10,33 +10,53 @@
 #include <algorithm>
 
 #include "cache_device.cuh"
+#include "ptx.cuh"
 #include "rotary_math.cuh"
+#include "softmax_math.cuh"
 #include "swa_host.h"
 
 namespace swa {
 namespace {
 
-constexpr int kRows = 64, kKeys = 64;      // tile of the CUDA-core kernel
+constexpr int kKeys = 64;                  // keys of a step of the CUDA-core kernel
 constexpr int kCoreThreads = 256;
 
-template <int D>
+template <int D, int RT>
 constexpr int core_smem_bytes() {
-  return (kRows * (D + 4) + kKeys * (D + 4) + kRows * (kKeys + 4)) * 4 + kKeys * 4;
+  constexpr int kRows = 16 * RT;
+  return (kRows * (D + 4) + 2 * kKeys * (D + 4) + kRows * (kKeys + 4)) * 4 + 2 * kKeys * 8;
 }
 
-// 64 rows x 64 keys a step in fp32 on the FMA pipe, each thread 4 x 4 scores and
-// 4 x D/16 outputs; K and V take turns in one shared buffer so that two blocks fit on
-// an SM and one computes while the other loads.
-template <int D>
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 16 RT rows x 64 keys a step in fp32 on the FMA pipe, each thread RT x 4 scores and RT x D/16
+// outputs (two products an instruction; reads of shared memory bound it, which more rows a
+// thread make fewer).  K of a step is fetched while V of the step before is used, and V
+// while K is, both with cp.async; where each key lies is looked up a step ahead, by one
+// thread a key.  The tile is the smallest of 16, 64 and 128 rows that the rows of a sequence
+// fill: 2 x 256 tokens of 40 heads, 8 KV heads, over 4096 keys, D = 128, take 1.40 ms with 128
+// (30 TFLOP/s) and 1.78 ms with 64 rows; one token of 8 sequences of 4000 keys 218 us with 16
+// and 370 us with 64.
+template <int D, int RT>
 __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_constant__ CacheAttendParams p,
                                                                   int row_tiles) {
+  constexpr int kRows = 16 * RT;
   constexpr int LD = D + 4, LP = kKeys + 4;
   constexpr int NC = D / 64;               // float4 columns of a thread
   extern __shared__ float smem[];
   float* sQ = smem;
-  float* sKV = sQ + kRows * LD;
-  float* sP = sKV + kKeys * LD;
-  int* sOk = reinterpret_cast<int*>(sP + kRows * LP);
+  float* sK = sQ + kRows * LD;
+  float* sV = sK + kKeys * LD;
+  float* sP = sV + kKeys * LD;
+  long long* sAt = reinterpret_cast<long long*>(sP + kRows * LP);   // [2][keys] element offset of a key, < 0: none
 
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int hk = blockIdx.y;
@@ -70,74 +90,88 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
   const int tiles = hi > lo ? (hi - lo + kKeys - 1) / kKeys : 0;
   const int j0 = (int)((long long)tiles * split / p.nsplit), j1 = (int)((long long)tiles * (split + 1) / p.nsplit);
 
-  int klo[4], khi[4];
+  int klo[RT], khi[RT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + ty * 4 + i;
+  for (int i = 0; i < RT; ++i) {
+    const int r = r0 + ty * RT + i;
     klo[i] = r < rows ? key_begin(p, s, r / p.G) : 0;
     khi[i] = r < rows ? key_end(s, r / p.G) : 0;
   }
-  float m[4], l[4], o[4][4 * NC];
+  float m[RT], l[RT], o[RT][4 * NC];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RT; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
     for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
   }
 
+  // a key exists if it lies in the tile's range and its page in the pool
+  auto look_up = [&](int j) {
+    if (tid >= kKeys) return;
+    const int pos = lo + j * kKeys + tid;
+    long long at = -1;
+    if (j < j1 && pos < hi) {
+      const int page = __ldg(p.block_table + (long long)b * p.max_pages + pos / p.page_size);
+      if (page >= 0 && page < p.num_pages)
+        at = (((long long)page * p.Hkv + hk) * p.page_size + pos % p.page_size) * D;
+      else
+        atomicOr(p.err, kDevErrCheck);
+    }
+    sAt[(j & 1) * kKeys + tid] = at;
+  };
+  auto fetch = [&](const void* pages, float* dst, int j) {         // zeros for a key that does not exist
+#pragma unroll
+    for (int e = tid; e < kKeys * (D / 4); e += kCoreThreads) {
+      const int k = e / (D / 4), c = e % (D / 4) * 4;
+      const long long at = sAt[(j & 1) * kKeys + k];
+      copy16(dst + k * LD + c, static_cast<const float*>(pages) + (at < 0 ? 0 : at) + c, at >= 0);
+    }
+    copy_commit();
+  };
+  if (j0 < j1) {
+    look_up(j0);
+    __syncthreads();
+    fetch(p.k_pages, sK, j0);
+    fetch(p.v_pages, sV, j0);
+  }
   for (int j = j0; j < j1; ++j) {
     const int key0 = lo + j * kKeys;
-    // a key exists if it lies in the tile's range and its page in the pool
-    auto load = [&](const void* pages, bool keys) {
-      for (int e = tid; e < kKeys * (D / 8); e += kCoreThreads) {
-        const int k = e / (D / 8), c = e % (D / 8) * 8;
-        const int pos = key0 + k;
-        float x[8];
-        bool ok = pos < hi;
-        if (ok) {
-          const int page = __ldg(p.block_table + (long long)b * p.max_pages + pos / p.page_size);
-          ok = page >= 0 && page < p.num_pages;
-          if (ok)
-            unpack(load_chunk(static_cast<const float*>(pages) +
-                              (((long long)page * p.Hkv + hk) * p.page_size + pos % p.page_size) * D + c), x);
-          else if (keys && c == 0) atomicOr(p.err, kDevErrCheck);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sKV[k * LD + c + i] = ok ? x[i] : 0.f;
-        if (keys && c == 0) sOk[k] = ok;
-      }
-    };
-    __syncthreads();                       // the previous step's V has been read
-    load(p.k_pages, true);
+    look_up(j + 1);
+    copy_wait<1>();                        // K of this step (V may be on its way)
     __syncthreads();
-    float sc[4][4];
+    float sc[RT][4], odd[RT][4];             // sums over even and odd d: two products an instruction
+    bool there[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int k = 0; k < 4; ++k) there[k] = sAt[(j & 1) * kKeys + tx + 16 * k] >= 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sc[i][k] = 0.f;
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sc[i][k] = odd[i][k] = 0.f;
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-      float4 q4[4], k4[4];
+      float4 q4[RT], k4[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q4[i] = *reinterpret_cast<const float4*>(sQ + (ty * 4 + i) * LD + d);
+      for (int i = 0; i < RT; ++i) q4[i] = *reinterpret_cast<const float4*>(sQ + (ty * RT + i) * LD + d);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) k4[k] = *reinterpret_cast<const float4*>(sKV + (tx + 16 * k) * LD + d);
+      for (int k = 0; k < 4; ++k) k4[k] = *reinterpret_cast<const float4*>(sK + (tx + 16 * k) * LD + d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          sc[i][k] += q4[i].x * k4[k].x + q4[i].y * k4[k].y + q4[i].z * k4[k].z + q4[i].w * k4[k].w;
+        for (int k = 0; k < 4; ++k) {
+          ffma2(sc[i][k], odd[i][k], q4[i].x, q4[i].y, k4[k].x, k4[k].y, sc[i][k], odd[i][k]);
+          ffma2(sc[i][k], odd[i][k], q4[i].z, q4[i].w, k4[k].z, k4[k].w, sc[i][k], odd[i][k]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RT; ++i) {
       float mx = m[i];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int pos = key0 + tx + 16 * k;
-        float x = sc[i][k] * p.scale;
+        float x = (sc[i][k] + odd[i][k]) * p.scale;
         if (p.softcap > 0.f) x = p.softcap * tanhf(x / p.softcap);
-        sc[i][k] = (pos >= klo[i] && pos < khi[i] && sOk[tx + 16 * k]) ? x : -INFINITY;
+        sc[i][k] = (pos >= klo[i] && pos < khi[i] && there[k]) ? x : -INFINITY;
         mx = fmaxf(mx, sc[i][k]);
       }
 #pragma unroll
@@ -149,7 +183,7 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float e = expf(sc[i][k] - ref);
-        sP[(ty * 4 + i) * LP + tx + 16 * k] = e;
+        sP[(ty * RT + i) * LP + tx + 16 * k] = e;
         sum += e;
       }
 #pragma unroll
@@ -159,34 +193,36 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
       for (int c = 0; c < 4 * NC; ++c) o[i][c] *= alpha;
     }
     __syncthreads();                       // K has been read, P is written
-    load(p.v_pages, false);
+    fetch(p.k_pages, sK, j + 1);           // behind the last step: zeros that nobody reads
+    copy_wait<1>();                        // V of this step
     __syncthreads();
 #pragma unroll 4
     for (int k = 0; k < kKeys; k += 4) {
-      float4 pr[4];
+      float4 pr[RT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4*>(sP + (ty * 4 + i) * LP + k);
+      for (int i = 0; i < RT; ++i) pr[i] = *reinterpret_cast<const float4*>(sP + (ty * RT + i) * LP + k);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          const float4 v = *reinterpret_cast<const float4*>(sKV + (k + kk) * LD + tx * 4 + 64 * c);
+          const float4 v = *reinterpret_cast<const float4*>(sV + (k + kk) * LD + tx * 4 + 64 * c);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < RT; ++i) {
             const float w = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
-            o[i][4 * c] += w * v.x;
-            o[i][4 * c + 1] += w * v.y;
-            o[i][4 * c + 2] += w * v.z;
-            o[i][4 * c + 3] += w * v.w;
+            ffma2(o[i][4 * c], o[i][4 * c + 1], w, w, v.x, v.y, o[i][4 * c], o[i][4 * c + 1]);
+            ffma2(o[i][4 * c + 2], o[i][4 * c + 3], w, w, v.z, v.w, o[i][4 * c + 2], o[i][4 * c + 3]);
           }
         }
       }
     }
+    __syncthreads();                       // V has been read
+    fetch(p.v_pages, sV, j + 1);
   }
+  copy_wait<0>();
 
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + ty * 4 + i;
+  for (int i = 0; i < RT; ++i) {
+    const int r = r0 + ty * RT + i;
     if (r >= rows) continue;
     const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
     const bool has = m[i] != -INFINITY;
@@ -246,13 +282,20 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ launches
-template <int D>
+template <int D, int RT>
 cudaError_t launch_core(const CacheAttendParams& p, int row_tiles, cudaStream_t s) {
-  cudaError_t e = allow_smem<&cache_core_kernel<D>>(core_smem_bytes<D>());
+  constexpr int smem = core_smem_bytes<D, RT>();
+  const cudaError_t e = allow_smem<&cache_core_kernel<D, RT>>(smem);
   if (e != cudaSuccess) return e;
-  cache_core_kernel<D><<<dim3((unsigned)((long long)p.B * row_tiles * p.nsplit), p.Hkv), kCoreThreads, core_smem_bytes<D>(), s>>>(
+  cache_core_kernel<D, RT><<<dim3((unsigned)((long long)p.B * row_tiles * p.nsplit), p.Hkv), kCoreThreads, smem, s>>>(
       p, row_tiles);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_core(const CacheAttendParams& p, int tile_rows, int row_tiles, cudaStream_t s) {
+  return tile_rows == 16 ? launch_core<D, 1>(p, row_tiles, s)
+         : tile_rows == 64 ? launch_core<D, 4>(p, row_tiles, s) : launch_core<D, 8>(p, row_tiles, s);
 }
 
 cudaError_t launch_merge(const CacheAttendParams& p, cudaStream_t s) {
@@ -268,7 +311,7 @@ struct AttendSplit {
   enum { kToken, kChunk, kCore } kernel;
   TokenSplit token;
   ChunkSplit chunk;
-  int row_tiles, nsplit;                   // CUDA-core kernel: tiles of rows, parts of the keys
+  int tile_rows, row_tiles, nsplit;        // CUDA-core kernel: rows of a tile, tiles, parts of the keys
   size_t bytes;                            // workspace
 };
 
@@ -292,11 +335,13 @@ AttendSplit attend_split(const swa_cache& c, const swa_cache_batch& b, const swa
     return r;
   }
   r.kernel = AttendSplit::kCore;
-  r.row_tiles = (int)(((long long)max_tokens * G + kRows - 1) / kRows);
-  // parts of at least 256 keys, two blocks an SM
+  const long long rows = (long long)max_tokens * G;
+  r.tile_rows = rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
+  r.row_tiles = (int)((rows + r.tile_rows - 1) / r.tile_rows);
+  // parts of a step of keys at least, two blocks an SM
   const long long blocks = (long long)b.batch * r.row_tiles * c.num_kv_heads;
   const long long want = (148 * 2 + blocks - 1) / std::max<long long>(blocks, 1);
-  r.nsplit = (int)std::max<long long>(1, std::min<long long>({want, reach / 256, 64}));
+  r.nsplit = (int)std::max<long long>(1, std::min<long long>({want, reach / kKeys, 64}));
   if (r.nsplit > 1) r.bytes = (size_t)r.nsplit * b.num_tokens * a.num_q_heads * (c.head_dim + 1) * 4;
   return r;
 }
@@ -412,7 +457,8 @@ swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const 
     p.part_o = static_cast<float*>(a->workspace);
     p.part_lse = p.part_o + (size_t)p.nsplit * p.T * p.Hq * p.D;
   }
-  e = p.D == 64 ? swa::launch_core<64>(p, sp.row_tiles, s) : swa::launch_core<128>(p, sp.row_tiles, s);
+  e = p.D == 64 ? swa::launch_core<64>(p, sp.tile_rows, sp.row_tiles, s)
+                : swa::launch_core<128>(p, sp.tile_rows, sp.row_tiles, s);
   if (e == cudaSuccess && p.nsplit > 1) e = swa::launch_merge(p, s);
   return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }

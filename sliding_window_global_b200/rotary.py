@@ -138,6 +138,11 @@ def head_norm(norm_eps, q_weight, k_weight, head_dim: int, device) -> HeadNorm:
     return HeadNorm(1, norm_eps, ptrs[0], ptrs[1], code)
 
 
+def check_start(start: int):
+    if not -2 ** 31 <= start < 2 ** 31:
+        raise ValueError(f"start must be an int32, got {start}")
+
+
 def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                        original_length: int = 4096, low_turns: float = 1.0, high_turns: float = 32.0):
     """Radians a position for each of the ``rotary_dim / 2`` pairs (fp64, on the host), and
@@ -216,6 +221,7 @@ class Rotary:
             return self._forward(q, k, positions, start, norm_eps, q_weight, k_weight, q_out, k_out)
 
     def _forward(self, q, k, positions, start, norm_eps, q_weight, k_weight, q_out, k_out):
+        check_start(start)
         device, dtype = q.device, q.dtype
         code = _dtype_code(dtype)
         qs = check_rows(q, "q", device, 4)
@@ -269,6 +275,7 @@ class Rotary:
             return self._backward(dq_out, dk_out, q, k, positions, start, norm_eps, q_weight, k_weight, dq, dk)
 
     def _backward(self, dq_out, dk_out, q, k, positions, start, norm_eps, q_weight, k_weight, dq, dk):
+        check_start(start)
         device = dq_out.device
         gs = check_rows(dq_out, "dq_out", device, 4)
         B, Hq, n, D = dq_out.shape

@@ -469,6 +469,40 @@ def test_offsets_beyond_32_bits():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("new", [[1, 2], [60, 3]])
+def test_bounds_beyond_int32(new):
+    """Windows, lengths and token bounds that no int32 length can reach bound nothing."""
+    s = _problem(BF16, 1, 64, 16, new, [90, 70], 27)
+    q = torch.randn((s["total"], 4, 64), generator=s["g"]).bfloat16().cuda()
+    args = (q, s["lens"].cuda(), s["table"].cuda())
+    want, _ = s["cache"].attend(*args, cu_tokens=s["cu"].cuda())
+    for big in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 40):
+        out, lse = s["cache"].attend(*args, cu_tokens=s["cu"].cuda(), window=big, max_len=big, max_tokens=big)
+        assert s["cache"].check() == 0
+        check_attention(out, lse, reference(s, q, None, 0.0, 0.0, 4), BF16)
+
+
+@pytest.mark.gpu
+def test_nothing_to_do():
+    """No sequences, no new tokens, sequences without any: nothing is written, nothing fails."""
+    s = _problem(BF16, 2, 64, 16, [0, 3, 0], [0, 3, 40], 31)
+    q, k = (torch.randn((3, h, 64), generator=s["g"]).bfloat16().cuda() for h in (4, 2))
+    lens, table, cu = s["lens"].cuda(), s["table"].cuda(), s["cu"].cuda()
+    before = s["k"].clone()
+    none = dict(cu_tokens=torch.zeros(4, dtype=torch.int32, device="cuda"))
+    assert s["cache"].append(k[:0], k[:0], lens, table, q=q[:0], **none).shape == (0, 4, 64)
+    assert s["cache"].attend(q[:0], lens, table, **none)[0].shape == (0, 4, 64)
+    s["cache"].append(k[:0], k[:0], lens[:0], table[:0])
+    assert s["cache"].attend(q[:0], lens[:0], table[:0])[1].shape == (0, 4)
+    assert torch.equal(s["k"], before)
+    out, lse = s["cache"].attend(q, lens, table, cu_tokens=cu, max_tokens=0)      # the call's own bound: no row
+    s["cache"].check()
+    out, lse = s["cache"].attend(q, lens, table, cu_tokens=cu, max_tokens=3)
+    assert s["cache"].check() == 0
+    check_attention(out, lse, reference(s, q, None, 0.0, 0.0, 4), BF16)
+
+
+@pytest.mark.gpu
 def test_shared_prefix_pages_and_scale():
     s = _problem(BF16, 2, 64, 16, [1, 1], [90, 90], 23)
     s["table"][1, :5] = s["table"][0, :5]                  # 80 shared positions

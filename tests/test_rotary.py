@@ -378,7 +378,7 @@ def test_gpu_refusals():
                  lambda: r.forward(q, q[:, :, :2]), lambda: r.forward(q[0]),
                  lambda: r.forward(q, q_weight=w), lambda: r.forward(q, norm_eps=1e-6, q_weight=w[:32]),
                  lambda: r.forward(q, positions=torch.zeros((1, 2), dtype=torch.int32, device="cuda")),
-                 lambda: r.forward(q, q_out=q[:, :1]), lambda: r.backward(q, norm_eps=1e-6),
+                 lambda: r.forward(q, q_out=q[:, :1]), lambda: r.forward(q, start=2 ** 31), lambda: r.backward(q, norm_eps=1e-6),
                  lambda: r.backward(q, None, q, q), lambda: r.backward(q, q, q, q[:, :1])):
         with pytest.raises(ValueError):
             call()
