@@ -182,7 +182,7 @@ class PagedCache:
                 raise ValueError("out must be contiguous")
         if lse is None:
             if return_lse:
-                lse = torch.empty((T, Hq), dtype=torch.float32, device=self._device)
+                lse = q.new_empty((T, Hq), dtype=torch.float32)
         elif lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous() or \
                 lse.device != self._device:
             raise ValueError(f"lse must be a contiguous fp32 [{T}, {Hq}] on {self._device}")

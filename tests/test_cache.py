@@ -303,6 +303,8 @@ ATTENDS = [
     ("many_short", BF16, 8, 4, 64, 16, None, 0.0, [1] * 50, [1 + 37 * i % 211 for i in range(50)]),
     ("many_uneven", BF16, 4, 1, 128, 64, None, 30.0, [1] * 40, [1 + 977 * i % 2999 for i in range(39)] + [12000]),
     ("cluster", BF16, 6, 1, 128, 16, 900, 0.0, [2, 1], [700, 2000]),
+    ("cluster_of_8", BF16, 8, 1, 128, 64, None, 0.0, [1], [1900]),
+    ("one_block_each", BF16, 12, 12, 64, 32, None, 0.0, [1] * 13, [1 + 31 * i for i in range(13)]),
     ("guesses", BF16, 10, 2, 128, 16, None, 0.0, [3] * 3, [3, 50, 517]),
     ("guesses_window", BF16, 40, 8, 64, 16, 17, 0.0, [8, 1, 5, 0], [8, 20, 300, 77]),
     ("wide_group", BF16, 24, 1, 64, 32, None, 0.0, [1, 2], [100, 400]),
@@ -408,6 +410,20 @@ def test_broken_bounds_stay_in_bounds(new):
     assert bool(((out[c:].float() - good[c:].float()).abs() <= 2.0 ** -6 * (1 + good[c:].float().abs())).all())
     st, out, lse = run(lens=torch.tensor([2 ** 31 - 1, 90], **i32))
     assert st == DEVICE_CHECK and bool(torch.isfinite(out[:c].float()).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,T,G", [(BF16, 6, 4), (BF16, 140, 4), (FP32, 20, 1)])
+def test_sequences_that_claim_the_same_rows(dtype, T, G):
+    """cu_tokens that go back to 0 name more rows than there are: in bounds, and reported."""
+    s = _problem(dtype, 2, 64, 16, [T, 0, T], [200, 10, 160], 37)
+    q = torch.randn((T, 2 * G, 64), generator=s["g"]).to(dtype).cuda()
+    cu = torch.tensor([0, T, 0, T], dtype=torch.int32, device="cuda")
+    out, lse = s["cache"].attend(q, s["lens"].cuda(), s["table"].cuda(), cu_tokens=cu, max_tokens=T)
+    assert s["cache"].check() == DEVICE_CHECK
+    k = torch.randn((T, 2, 64), generator=s["g"]).to(dtype).cuda()
+    s["cache"].append(k, k, s["lens"].cuda(), s["table"].cuda(), cu_tokens=cu)
+    s["cache"].check()
 
 
 @pytest.mark.gpu
