@@ -25,12 +25,14 @@ namespace {
 constexpr int kRotaryThreads = 128;
 // Heads of a block at most. Forward, a 2 x 8191-token normed prompt: 57.5 us with 32, 59.7 with
 // 16. Backward, a normed 16384-token prompt: 131 us with 16, whose items the blocks share
-// out evenly, 134 with 8, 143 with 32.
+// out evenly, 134 with 8, 143 with 32 (before the products went two an instruction: 56.0 and
+// 129 us now).
 constexpr int kForwardRun = 32, kBackwardRun = 16;
 // Blocks of an SM that the registers must allow. Forward: four (128 registers; 104.5 us for
 // the plain 32768-token prompt, 106.7 without the bound). Backward: five without a norm; with
 // one the compiler's own choice of 168 registers, since four blocks would spill (131 to 163 us).
-constexpr int kForwardBlocks = 4, kBackwardBlocks = 5;
+// Append: three, whose look-ups need more registers (normed prompts 45.9 us, 51.6 with four).
+constexpr int kForwardBlocks = 4, kBackwardBlocks = 5, kAppendBlocks = 3;
 
 template <typename T>
 __host__ __device__ constexpr int unroll_heads() {
@@ -105,7 +107,7 @@ __device__ __forceinline__ CacheToken cache_token(const RotaryParams& p, int tok
 }
 
 template <typename T, int D, bool NORM, bool INTER, bool CACHE>
-__global__ void __launch_bounds__(kRotaryThreads, kForwardBlocks) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kRotaryThreads, CACHE ? kAppendBlocks : kForwardBlocks) rotary_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int kPer = D / 16;                             // threads of a row
   constexpr int U = unroll_heads<T>();
   const int th = threadIdx.x % kPer;
@@ -175,14 +177,13 @@ __global__ void __launch_bounds__(kRotaryThreads, kForwardBlocks) rotary_kernel(
         unpack(a[u], xa);
         unpack(b[u], xb);
         if (NORM) {
-          float ss = 0.f;
+          const float inv = __frsqrt_rn(row_sum<D>(squares(xa, xb)) * (1.f / D) + p.m.eps);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
-          const float inv = __frsqrt_rn(row_sum<D>(ss) * (1.f / D) + p.m.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            xa[i] = xa[i] * inv * wa[i];
-            xb[i] = xb[i] * inv * wb[i];
+          for (int i = 0; i < 8; i += 2) {
+            fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], inv, inv);
+            fmul2(xa[i], xa[i + 1], xa[i], xa[i + 1], wa[i], wa[i + 1]);
+            fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], inv, inv);
+            fmul2(xb[i], xb[i + 1], xb[i], xb[i + 1], wb[i], wb[i + 1]);
           }
         }
         rotate<INTER, false>(xa, xb, cp, cs, sn);
@@ -283,29 +284,29 @@ __global__ void __launch_bounds__(kRotaryThreads, NORM ? 1 : kBackwardBlocks) ro
           float ua[8], ub[8];
           unpack(xa[u], ua);
           unpack(xb[u], ub);
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss += ua[i] * ua[i] + ub[i] * ub[i];
-          const float inv = __frsqrt_rn(row_sum<D>(ss) * (1.f / D) + p.m.eps);
+          const float inv = __frsqrt_rn(row_sum<D>(squares(ua, ub)) * (1.f / D) + p.m.eps);
           const bool live = ok && h0 + u < he;             // a row of zeros with eps 0 has no norm
-          float dot = 0.f;
+          float d0 = 0.f, d1 = 0.f, e0 = 0.f, e1 = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ua[i] *= inv;
-            ub[i] *= inv;
+          for (int i = 0; i < 8; i += 2) {
+            fmul2(ua[i], ua[i + 1], ua[i], ua[i + 1], inv, inv);
+            fmul2(ub[i], ub[i + 1], ub[i], ub[i + 1], inv, inv);
             if (live) {
-              da[i] += ha[i] * ua[i];
-              db[i] += hb[i] * ub[i];
+              ffma2(da[i], da[i + 1], ha[i], ha[i + 1], ua[i], ua[i + 1], da[i], da[i + 1]);
+              ffma2(db[i], db[i + 1], hb[i], hb[i + 1], ub[i], ub[i + 1], db[i], db[i + 1]);
             }
-            ha[i] *= wa[i];
-            hb[i] *= wb[i];
-            dot += ha[i] * ua[i] + hb[i] * ub[i];
+            fmul2(ha[i], ha[i + 1], ha[i], ha[i + 1], wa[i], wa[i + 1]);
+            fmul2(hb[i], hb[i + 1], hb[i], hb[i + 1], wb[i], wb[i + 1]);
+            ffma2(d0, d1, ha[i], ha[i + 1], ua[i], ua[i + 1], d0, d1);
+            ffma2(e0, e1, hb[i], hb[i + 1], ub[i], ub[i + 1], e0, e1);
           }
-          dot = row_sum<D>(dot) * (1.f / D);
+          const float dot = -row_sum<D>((d0 + d1) + (e0 + e1)) * (1.f / D);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            ha[i] = inv * (ha[i] - ua[i] * dot);
-            hb[i] = inv * (hb[i] - ub[i] * dot);
+          for (int i = 0; i < 8; i += 2) {
+            ffma2(ha[i], ha[i + 1], ua[i], ua[i + 1], dot, dot, ha[i], ha[i + 1]);
+            ffma2(hb[i], hb[i + 1], ub[i], ub[i + 1], dot, dot, hb[i], hb[i + 1]);
+            fmul2(ha[i], ha[i + 1], ha[i], ha[i + 1], inv, inv);
+            fmul2(hb[i], hb[i + 1], hb[i], hb[i + 1], inv, inv);
           }
         }
         if (ok && h0 + u < he) {

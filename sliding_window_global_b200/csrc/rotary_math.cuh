@@ -12,6 +12,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "softmax_math.cuh"
+
 namespace swa {
 
 constexpr int kMaxPairs = 64;              // rotated pairs of a head (head_dim <= 128)
@@ -106,13 +108,28 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Chunk
     }
   } else if (cp.ra) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = BACK ? -sn[i] : sn[i];
-      const float x = a[i], y = b[i];
-      a[i] = x * cs[i] - y * s;
-      b[i] = x * s + y * cs[i];
+    for (int i = 0; i < 8; i += 2) {       // two pairs an instruction
+      float x0, x1, y0, y1;
+      const float s0 = BACK ? -sn[i] : sn[i], s1 = BACK ? -sn[i + 1] : sn[i + 1];
+      fmul2(x0, x1, b[i], b[i + 1], -s0, -s1);
+      fmul2(y0, y1, a[i], a[i + 1], s0, s1);
+      ffma2(x0, x1, a[i], a[i + 1], cs[i], cs[i + 1], x0, x1);
+      ffma2(b[i], b[i + 1], b[i], b[i + 1], cs[i], cs[i + 1], y0, y1);
+      a[i] = x0;
+      a[i + 1] = x1;
     }
   }
+}
+
+// Sum of the squares of a thread's elements.
+__device__ __forceinline__ float squares(const float (&a)[8], const float (&b)[8]) {
+  float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    ffma2(s0, s1, a[i], a[i + 1], a[i], a[i + 1], s0, s1);
+    ffma2(t0, t1, b[i], b[i + 1], b[i], b[i + 1], t0, t1);
+  }
+  return (s0 + s1) + (t0 + t1);
 }
 
 // Sum over the D / 16 threads of a row (every lane of the warp takes part).
