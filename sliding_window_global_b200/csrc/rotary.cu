@@ -470,7 +470,10 @@ swa_status make_rotary_math(const swa_rotation& r, const swa_head_norm& n, int D
   if (r.rotary_dim % 16 != 0) return SWA_ERR_UNSUPPORTED;
   for (int i = 0; i < r.rotary_dim / 2; ++i) {
     if (!isfinite(r.freq[i])) return SWA_ERR_INVALID_ARG;
-    m->quarter[i] = r.freq[i] * 0.63661977236758134308;    // 2 / pi
+    // turns modulo one, as a fraction of 2^64
+    const long double turns = static_cast<long double>(r.freq[i]) * 0.159154943091895335768883763372514362L;
+    const long double part = turns - floorl(turns);
+    m->turn[i] = part >= 1.0L ? 0 : static_cast<uint64_t>(ldexpl(part, 64));
   }
   m->amp = r.amplitude == 0.f ? 1.f : r.amplitude;
   m->eps = n.norm ? n.eps : 0.f;

@@ -21,22 +21,45 @@ constexpr int kMaxPairs = 64;              // rotated pairs of a head (head_dim 
 // What every kernel that rotates or norms head rows needs of swa_rotation and
 // swa_head_norm.
 struct RotaryMath {
-  double quarter[kMaxPairs];               // quarter turns per position of each pair
+  uint64_t turn[kMaxPairs];                // turns per position of each pair, in units of 2^-64, modulo one turn
   float amp;
   float eps;
   int rot;                                 // R
   int weight_bf16;                         // element type of the norm's weights
 };
 
-// cos and sin of t * freq.  The angle in quarter turns is formed and reduced in 64
-// bits (positions reach millions, where 32 bits would leave no digit of the angle);
-// its rest in [-1/2, 1/2] is rounded to 32 bits, an error below 2^-25 * pi / 2.
-__device__ __forceinline__ void rotary_angle(int t, double quarter, float amp, float& c, float& s) {
-  const double turn = static_cast<double>(t) * quarter;
-  const double whole = rint(turn);
+// sin and cos of pi x for |x| <= 1/4, by their series: the first terms left out are below
+// (pi / 4)^11 / 11! = 1.8e-9 and (pi / 4)^12 / 12! = 1.2e-10.
+__device__ __forceinline__ void sincos_quarter(float x, float& s, float& c) {
+  constexpr double kPi = 3.14159265358979323846, kPi2 = kPi * kPi;
+  constexpr double kPi4 = kPi2 * kPi2, kPi6 = kPi4 * kPi2, kPi8 = kPi4 * kPi4;
+  constexpr float pi_hi = static_cast<float>(kPi), pi_lo = static_cast<float>(kPi - static_cast<double>(pi_hi));
+  const float y = x * x;
+  float p = static_cast<float>(kPi8 * kPi / 362880);
+  p = fmaf(p, y, static_cast<float>(-kPi6 * kPi / 5040));
+  p = fmaf(p, y, static_cast<float>(kPi4 * kPi / 120));
+  p = fmaf(p, y, static_cast<float>(-kPi2 * kPi / 6));
+  p = fmaf(p, y, pi_lo);
+  s = fmaf(x, pi_hi, x * p);
+  float q = static_cast<float>(-kPi8 * kPi2 / 3628800);
+  q = fmaf(q, y, static_cast<float>(kPi8 / 40320));
+  q = fmaf(q, y, static_cast<float>(-kPi6 / 720));
+  q = fmaf(q, y, static_cast<float>(kPi4 / 24));
+  q = fmaf(q, y, static_cast<float>(-kPi2 / 2));
+  c = fmaf(q, y, 1.f);
+}
+
+// cos and sin of t * freq, times amp. The position is a whole number, so the angle in turns
+// can be formed modulo one in fixed point, exactly but for the frequency's own rounding to
+// 2^-65 turns: with t below 2^31 an error below 2^-34 turns. (32-bit floats would leave
+// no digit of it at far positions, and 64-bit ones are slow.) The rest to the nearest
+// quarter turn is cut to 2^-32 turns and rounded to 24 bits, an error below 2^-25.
+__device__ __forceinline__ void rotary_angle(int t, uint64_t turn, float amp, float& c, float& s) {
+  const uint32_t at = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<int64_t>(t)) * turn) >> 32);
+  const uint32_t k = (at + 0x20000000u) >> 30;             // nearest quarter turn
+  const int rest = static_cast<int>(at - (k << 30));
   float sf, cf;
-  sincospif(0.5f * static_cast<float>(turn - whole), &sf, &cf);
-  const int k = static_cast<int>(static_cast<long long>(whole)) & 3;
+  sincos_quarter(static_cast<float>(rest) * 0x1p-31f, sf, cf);
   const float cr = (k & 1) ? sf : cf;
   const float sr = (k & 1) ? cf : sf;
   c = (k == 1 || k == 2) ? -cr * amp : cr * amp;
@@ -78,7 +101,7 @@ __device__ __forceinline__ void rotary_table(const RotaryMath& m, const ChunkPai
     const int j = INTER ? (i < 4 ? 4 * cp.a + i : 4 * cp.b + i - 4) : 8 * cp.a + i;
     cs[i] = 1.f;
     sn[i] = 0.f;
-    if (on) rotary_angle(t, m.quarter[j], m.amp, cs[i], sn[i]);
+    if (on) rotary_angle(t, m.turn[j], m.amp, cs[i], sn[i]);
   }
 }
 
