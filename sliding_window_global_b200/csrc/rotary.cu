@@ -483,8 +483,10 @@ swa_status make_rotary_math(const swa_rotation& r, const swa_head_norm& n, int D
 }
 
 int split_heads(long long token_tiles, const int* heads, int kinds, int longest, int* segs) {
-  // Longer runs of heads reuse a token's cosines; shorter ones make more blocks.  Halve
-  // the runs until the call has eight blocks an SM.
+  // Longer runs of heads reuse a token's cosines and keep loads in flight; shorter ones make
+  // more blocks. Halve the runs until the call has two blocks an SM. Measured with two and
+  // with eight: 8 + 2 normed heads of 5935 tokens 10.6 and 16.6 us, 64 sequences of 8 new tokens
+  // 8.4 and 12.5 us, gradients of 16 + 8 normed heads of 7 x 435 tokens 18.6 and 24.7 us.
   int per = 1;
   for (int i = 0; i < kinds; ++i)
     while (per < heads[i] && per < longest) per *= 2;
@@ -494,7 +496,7 @@ int split_heads(long long token_tiles, const int* heads, int kinds, int longest,
       segs[i] = (heads[i] + per - 1) / per;
       blocks += token_tiles * segs[i];
     }
-    if (per == 1 || blocks >= 148 * 8) return per;
+    if (per == 1 || blocks >= 148 * 2) return per;
     per /= 2;
   }
 }
