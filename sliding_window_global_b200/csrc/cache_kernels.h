@@ -68,8 +68,10 @@ cudaError_t launch_cache_token(CacheAttendParams p, const TokenSplit& t, void* w
 struct ChunkSplit {
   int runs;                         // blocks, each with an equal run of key tiles
   int tile_tokens;                  // tokens of a query tile: 128 rows / heads of a group
+  int unit_tokens;                  // tokens of a unit: one query tile's or two's
+  bool direct;                      // a block a unit, no list of work
   int box;                          // keys of one load: they lie in one page
-  int max_entries;                  // token tiles of all sequences
+  int max_entries;                  // units of all sequences, for one KV head
   bool split;                       // units long enough to be parted between blocks
   size_t bytes;                     // workspace
 };
