@@ -139,11 +139,14 @@ __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
   return x;
 }
-__device__ __forceinline__ float2 ld_cluster2(const float* p, uint32_t rank) {
+__device__ __forceinline__ float4 ld_cluster4(const float* p, uint32_t rank) {
   uint32_t at;
-  float2 x;
+  float4 x;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(at)
+               : "memory");
   return x;
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -160,6 +163,7 @@ __device__ __forceinline__ void join_unit(const CacheAttendParams& p, const Cach
                                           float (&l)[MT][2]) {
   constexpr int R = 16 * MT, LD = D + 8;               // rows 32 bytes apart in the banks
   __shared__ float sM[kMaxWarps][R], sL[kMaxWarps][R], sTop[R], sSum[R];
+  __shared__ float sTops[8][R], sSums[8][R];           // the blocks' of the cluster
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, wb = blockDim.x >> 5;
   float* parts = reinterpret_cast<float*>(smem);       // [warps][R][LD]
   cp_async_wait<0>();
@@ -183,55 +187,63 @@ __device__ __forceinline__ void join_unit(const CacheAttendParams& p, const Cach
     }
   }
   __syncthreads();
-  const int pairs = rows * (D / 2);
-  auto store = [&](int i, float2 acc, float top, float sum) {
-    const int r = i / (D / 2), c = i % (D / 2) * 2;
-    const bool has = top != -INFINITY;
-    const float inv = has ? 1.f / sum : 0.f;
-    const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
-    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + row * D + c) = pack_bf16x2(acc.x * inv, acc.y * inv);
-    if (p.lse && c == 0) p.lse[row] = has ? (top + log2f(sum)) * kLn2 : -INFINITY;
-  };
-  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-    const int r = i / (D / 2), c = i % (D / 2) * 2;
-    float top = -INFINITY, sum = 0.f;
-    float2 acc = make_float2(0.f, 0.f);
-    for (int k = 0; k < wb; ++k) top = fmaxf(top, sM[k][r]);
-    for (int k = 0; k < wb; ++k) {
-      if (sM[k][r] == -INFINITY) continue;             // no key in this part (a NaN sum goes on)
-      const float f = ex2_approx(sM[k][r] - top);
-      const float2 x = *reinterpret_cast<const float2*>(parts + (k * R + r) * LD + c);
-      sum += f * sL[k][r];
-      acc.x += f * x.x;
-      acc.y += f * x.y;
-    }
-    if (cluster == 1) {
-      store(i, acc, top, sum);
-    } else {
-      *reinterpret_cast<float2*>(parts + r * LD + c) = acc;      // over warp 0's part: read by this thread alone
-      if (c == 0) {
-        sTop[r] = top;
-        sSum[r] = sum;
+  // each row's maximum and sum over n parts, and in place of their maxima the parts' weights
+  // (0 for a part without keys; a NaN sum goes on)
+  auto weigh = [&](float (*top)[R], float (*sum)[R], int n) {
+    if ((int)threadIdx.x < rows) {
+      const int r = threadIdx.x;
+      float t = -INFINITY, total = 0.f;
+      for (int k = 0; k < n; ++k) t = fmaxf(t, top[k][r]);
+      for (int k = 0; k < n; ++k) {
+        const float f = top[k][r] == -INFINITY ? 0.f : ex2_approx(top[k][r] - t);
+        top[k][r] = f;
+        total += f * sum[k][r];
       }
+      sTop[r] = t;
+      sSum[r] = total;
     }
+    __syncthreads();
+  };
+  constexpr int Q = D / 4;                             // 16-byte pieces of a row
+  auto store = [&](int r, int c, float4 acc) {
+    const bool has = sTop[r] != -INFINITY;
+    const float inv = has ? 1.f / sSum[r] : 0.f;
+    const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + c) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (p.lse && c == 0) p.lse[row] = has ? (sTop[r] + log2f(sSum[r])) * kLn2 : -INFINITY;
+  };
+  weigh(sM, sL, wb);
+  for (int i = threadIdx.x; i < rows * Q; i += blockDim.x) {
+    const int r = i / Q, c = i % Q * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < wb; ++k) {
+      const float f = sM[k][r];
+      const float4 x = *reinterpret_cast<const float4*>(parts + (k * R + r) * LD + c);
+      acc = make_float4(acc.x + f * x.x, acc.y + f * x.y, acc.z + f * x.z, acc.w + f * x.w);
+    }
+    if (cluster == 1) store(r, c, acc);
+    else *reinterpret_cast<float4*>(parts + r * LD + c) = acc;   // over warp 0's part: read by this thread alone
   }
   if (cluster == 1) return;
   cluster_sync();
-  for (int i = cluster_rank() * blockDim.x + threadIdx.x; i < pairs; i += cluster * blockDim.x) {
-    const int r = i / (D / 2), c = i % (D / 2) * 2;
-    float top = -INFINITY, sum = 0.f;
-    float2 acc = make_float2(0.f, 0.f);
-    for (int k = 0; k < cluster; ++k) top = fmaxf(top, ld_cluster(&sTop[r], k));
+  for (int i = threadIdx.x; i < cluster * rows; i += blockDim.x) {
+    sTops[i / rows][i % rows] = ld_cluster(&sTop[i % rows], i / rows);
+    sSums[i / rows][i % rows] = ld_cluster(&sSum[i % rows], i / rows);
+  }
+  cluster_sync();                                      // sTop and sSum are read before they are written again
+  weigh(sTops, sSums, cluster);
+  for (int i = cluster_rank() * blockDim.x + threadIdx.x; i < rows * Q; i += cluster * blockDim.x) {
+    const int r = i / Q, c = i % Q * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int k = 0; k < cluster; ++k) {
-      const float t = ld_cluster(&sTop[r], k);
-      if (t == -INFINITY) continue;
-      const float f = ex2_approx(t - top);
-      const float2 x = ld_cluster2(parts + r * LD + c, k);
-      sum += f * ld_cluster(&sSum[r], k);
-      acc.x += f * x.x;
-      acc.y += f * x.y;
+      const float f = sTops[k][r];
+      const float4 x = ld_cluster4(parts + r * LD + c, k);
+      acc = make_float4(acc.x + f * x.x, acc.y + f * x.y, acc.z + f * x.z, acc.w + f * x.w);
     }
-    store(i, acc, top, sum);
+    store(r, c, acc);
   }
   cluster_sync();                                      // nobody leaves while its memory is read
 }
@@ -541,15 +553,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
   cp_async_wait<0>();
 }
 
-// Joins the parts of every row whose unit was split: one block a row, its warps take the
-// parts in turn and are added up in order, so the same call gives the same bits.
-template <int D>
-__global__ void __launch_bounds__(128) cache_token_merge_kernel(const __grid_constant__ CacheAttendParams p, int W,
-                                                                 int row_pad) {
-  constexpr int E = D / 32;
-  __shared__ float sO[4][D], sM[4], sL[4];
+// Joins the parts of every row whose unit was split, a block a row: the parts' weights first,
+// then its warps add up the parts in turn, and the warps are added up in order, so the same
+// call gives the same bits. A unit has a part in every run that holds some of its steps, at
+// most all of them: blocks of 16 warps where the units are few, of four where they are many.
+template <int D, int kMergeThreads>
+__global__ void __launch_bounds__(kMergeThreads) cache_token_merge_kernel(const __grid_constant__ CacheAttendParams p,
+                                                                           int W, int row_pad) {
+  constexpr int kWarps = kMergeThreads / 32, E = D / 32;
+  __shared__ float sW[148 * kMaxWarps], sRed[kWarps], sSum[kWarps], sO[kWarps][D];
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int max_rows = p.max_tokens * p.G;
   const int r = blockIdx.x % max_rows;
   const int hk = blockIdx.x / max_rows % p.Hkv;
@@ -560,48 +573,61 @@ __global__ void __launch_bounds__(128) cache_token_merge_kernel(const __grid_con
   const int u0 = first + hk * steps, u1 = u0 + steps;
   // the runs that hold the unit's first and last step (none between them is empty)
   const Runs runs(n, W);
-  const int w0 = runs.of(u0), w1 = runs.of(u1 - 1);
-  if (w0 == w1) return;                    // stored whole
-  float m = -INFINITY, l = 0.f, o[E];
+  const int w0 = runs.of(u0), parts = runs.of(u1 - 1) - w0 + 1;
+  if (parts == 1) return;                  // stored whole
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // part k lies in slot 0 of its run, the first one in slot 1 (its unit began there)
+  auto row_of = [&](int k) { return (2LL * (w0 + k) + (k == 0 ? 1 : 0)) * row_pad + r; };
+  float top = -INFINITY;
+  for (int k = threadIdx.x; k < parts; k += kMergeThreads) {
+    sW[k] = p.part_lse[row_of(k)];
+    top = fmaxf(top, sW[k]);
+  }
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) sRed[warp] = top;
+  __syncthreads();
+  for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sRed[i]);
+  float sum = 0.f;
+  for (int k = threadIdx.x; k < parts; k += kMergeThreads) {
+    const float f = sW[k] == -INFINITY ? 0.f : ex2_approx((sW[k] - top) * kLog2e);   // no key: 0 (a NaN goes on)
+    sW[k] = f;
+    sum += f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) sSum[warp] = sum;
+  __syncthreads();
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int w = w0 + wp; w <= w1; w += 4) {
-    const long long row = (2LL * w + (w == w0 ? 1 : 0)) * row_pad + r;
-    const float lse = p.part_lse[row];
-    float x[E];
+  for (int k = warp; k < parts; k += kWarps) {
+    const float f = sW[k];
+    const float2* src = reinterpret_cast<const float2*>(p.part_o + row_of(k) * D) + lane;
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = p.part_o[row * D + lane + 32 * e];
-    if (lse == -INFINITY) continue;        // no key in this part (a NaN goes on)
-    const float mx = fmaxf(m, lse);
-    const float keep = m == -INFINITY ? 0.f : ex2_approx((m - mx) * kLog2e), f = ex2_approx((lse - mx) * kLog2e);
-    m = mx;
-    l = l * keep + f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + f * x[e];
+    for (int e = 0; e < E; e += 2) {
+      const float2 x = src[16 * e];
+      acc[e] += f * x.x;
+      acc[e + 1] += f * x.y;
+    }
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) sO[wp][lane + 32 * e] = o[e];
-  if (lane == 0) {
-    sM[wp] = m;
-    sL[wp] = l;
-  }
+  for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(&sO[warp][32 * e + 2 * lane]) = make_float2(acc[e], acc[e + 1]);
   __syncthreads();
   if (threadIdx.x >= D) return;
-  float top = -INFINITY, sum = 0.f, acc = 0.f;
+  const int c = threadIdx.x;
+  float out = 0.f;
+  sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = fmaxf(top, sM[i]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (sL[i] == 0.f) continue;
-    const float f = ex2_approx((sM[i] - top) * kLog2e);
-    sum += f * sL[i];
-    acc += f * sO[i][threadIdx.x];
+  for (int i = 0; i < kWarps; ++i) {
+    out += sO[i][c];
+    sum += sSum[i];
   }
   const bool has = sum != 0.f;
   const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
-  static_cast<__nv_bfloat16*>(p.out)[row * D + threadIdx.x] = __float2bfloat16_rn(has ? acc / sum : 0.f);
-  if (p.lse && threadIdx.x == 0) p.lse[row] = has ? top + log2f(sum) * kLn2 : -INFINITY;
+  static_cast<__nv_bfloat16*>(p.out)[row * D + c] = __float2bfloat16_rn(has ? out / sum : 0.f);
+  if (p.lse && c == 0) p.lse[row] = has ? top + log2f(sum) * kLn2 : -INFINITY;
 }
 
 template <int D, int MT, bool CAP>
@@ -629,10 +655,12 @@ cudaError_t launch_token(const CacheAttendParams& p, const TokenSplit& t, cudaSt
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.max_tokens * p.G));
-  cfg.blockDim = dim3(128);
+  const bool many = (long long)p.B * p.Hkv * 16 > t.blocks * t.warps;      // fewer than 16 parts a unit
+  cfg.blockDim = dim3(many ? 128 : 512);
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, cache_token_merge_kernel<D>, p, t.blocks * t.warps, 16 * MT);
+  return cudaLaunchKernelEx(&cfg, many ? cache_token_merge_kernel<D, 128> : cache_token_merge_kernel<D, 512>, p,
+                            t.blocks * t.warps, 16 * MT);
 }
 
 // Shared memory of the joined parts fits into the rings they replace.
@@ -652,14 +680,16 @@ TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach) {
   // least; with more units than SMs, blocks of four warps, two of them on an SM.
   int cluster = 1, warps = units > 148 ? 4 : kMaxWarps;
   while (cluster < 8 && units * cluster * 2 <= 148 && unit_steps > cluster * warps * 2) cluster *= 2;
-  while (warps > 1 && unit_steps <= warps) warps /= 2;
+  if (unit_steps <= 4) warps = 4;        // not fewer: they share the join of the rows too
   const long long slots = 148 * (kMaxWarps / warps);
   const long long waves = (units * cluster + slots - 1) / slots;
-  const long long per_unit = waves * ((unit_steps + cluster * warps - 1) / (cluster * warps));
-  // Equal runs of all steps: better balanced, but a launch and a search more (about six
-  // steps' time).
+  // Equal runs of all steps: balanced whatever the lengths, but a launch and a search more
+  // (about six steps' time). Lengths may be anything below the bound, so that clusters are
+  // for few steps a warp only: three sequences of 4000 to 9656 keys, 12 heads, D = 128, take
+  // 37 us in runs and 44 us with clusters of four blocks, of 19 steps a warp.
+  const long long per_warp = (unit_steps + cluster * warps - 1) / (cluster * warps);
   const long long per_run = (steps + 148 * kMaxWarps - 1) / (148 * kMaxWarps);
-  if (per_unit <= per_run + 6 && units * cluster < (1LL << 31)) {
+  if (per_warp <= 16 && waves * per_warp <= per_run + 6 && units * cluster < (1LL << 31)) {
     t.cluster = cluster;
     t.warps = warps;
     t.blocks = (int)(units * cluster);
