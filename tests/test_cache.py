@@ -314,6 +314,9 @@ ATTENDS = [
     ("chunk_cap", BF16, 12, 12, 64, 128, None, 20.0, [140], [290]),
     ("chunk_self", BF16, 3, 1, 128, 32, 0, 0.0, [64, 65], [64, 100]),
     ("chunk_long", BF16, 4, 1, 128, 128, None, 0.0, [260], [3001]),
+    ("sequences_600", BF16, 2, 1, 64, 16, None, 0.0, [1] * 600, [1 + 7 * i % 41 for i in range(600)]),
+    ("sequences_600_rows_40", BF16, 8, 1, 64, 16, 20, 0.0, [5] * 599 + [6], [6 + 7 * i % 41 for i in range(600)]),
+    ("heads_128", BF16, 128, 1, 64, 32, None, 0.0, [3], [77]),
     ("fp32_tokens", FP32, 12, 12, 64, 16, None, 0.0, [1, 1], [300, 7]),
     ("fp32_long", FP32, 4, 1, 128, 64, None, 30.0, [2], [3000]),
     ("fp32_chunk", FP32, 6, 2, 64, 48, 50, 0.0, [100, 1, 0, 13], [170, 3, 9, 13]),
@@ -577,6 +580,73 @@ def test_a_layer_from_prompt_to_tokens():
     for got, ref in zip((gq, gk, gqw, gkw), want):
         # the attention backward's own bound: 2e-2 of the largest gradient
         assert float((got.double().cpu() - ref).abs().max()) <= 2e-2 * float(ref.abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [None, 40])
+def test_decoding_loop_in_a_graph(window):
+    """One captured step (append, attend, lengths moved on) replayed token after token, against
+    the attention of the whole sequences in 64 bits."""
+    B, Hq, Hkv, D, page, n = 3, 8, 2, 64, 16, 37
+    g = torch.Generator().manual_seed(43)
+    pages = torch.zeros((B * 6, Hkv, page, D), dtype=BF16, device="cuda")
+    cache = PagedCache(pages, torch.zeros_like(pages))
+    table = torch.randperm(B * 6, generator=g).view(B, 6).to(torch.int32)
+    start = torch.tensor([0, 11, 50], dtype=torch.int32)
+    qkv = torch.randn((B, int(start.max()) + n, Hq + 2 * Hkv, D), generator=g).bfloat16().cuda()
+    rot, dev = Rotary(D), table.cuda()
+    for b in range(B):                                     # what came before the loop
+        c = int(start[b])
+        if c:
+            rows = qkv[b, :c]
+            cache.append(rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:], start[b:b + 1].cuda(), dev[b:b + 1], rotary=rot)
+    lens = start.cuda()
+    new = torch.empty((B, Hq + 2 * Hkv, D), dtype=BF16, device="cuda")
+
+    def step():
+        lens.add_(1)
+        q = cache.append(new[:, Hq:Hq + Hkv], new[:, Hq + Hkv:], lens, dev, q=new[:, :Hq], rotary=rot)
+        return (q,) + cache.attend(q, lens, dev, window=window)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            q, out, lse = step()
+        got = []
+        for t in range(n):
+            new.copy_(torch.stack([qkv[b, int(start[b]) + t] for b in range(B)]))
+            graph.replay()
+            got.append((q.clone(), out.clone(), lse.clone()))
+    torch.cuda.synchronize()
+    assert cache.check() == 0 and torch.equal(lens.cpu(), start + n)
+    for t in (0, 1, n // 2, n - 1):
+        s = dict(k=cache.k_pages, v=cache.v_pages, page=page, table=table, lens=start + t + 1, new=[1] * B,
+                 cu=torch.arange(B + 1), total=B)
+        check_attention(got[t][1], got[t][2], reference(s, got[t][0], window, 0.0, 0.0, Hq), BF16)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU share nothing: each has its own workspace."""
+    cases = []
+    for new, lens, seed in (([1, 1], [9000, 4000], 47), ([300, 20], [2500, 20], 53)):
+        s = _problem(BF16, 2, 128, 64, new, lens, seed)
+        q = torch.randn((s["total"], 8, 128), generator=s["g"]).bfloat16().cuda()
+        args = (q, s["lens"].cuda(), s["table"].cuda())
+        kw = dict(cu_tokens=s["cu"].cuda(), max_tokens=max(new))
+        cases.append((s["cache"], args, kw, s["cache"].attend(*args, **kw), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    res = [[], []]
+    for _ in range(20):
+        for i, (cache, args, kw, _, stream) in enumerate(cases):
+            res[i].append(cache.attend(*args, stream=stream, **kw))
+    torch.cuda.synchronize()
+    for i, (cache, _, _, want, _) in enumerate(cases):
+        assert cache.check() == 0
+        for out, lse in res[i]:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 @pytest.mark.gpu
