@@ -10,8 +10,8 @@ from typing import Optional
 
 import torch
 
-from .rotary import (_NO_ROTATION, F, I, I64, P, HeadNorm, Rotary, Rotation, check_index, check_rows,
-                     current_stream, elsewhere, head_norm)
+from .rotary import (F, I, I64, NO_ROTATION, P, HeadNorm, Rotary, Rotation, check_index, check_rows, current_stream,
+                     elsewhere, head_norm, packer)
 from .swa import SwaError, _dtype_code, load_library
 
 
@@ -45,6 +45,7 @@ class CacheAttendArgs(ctypes.Structure):
     ]
 
 
+_pack_batch, _pack_append, _pack_attend = packer(CacheBatch), packer(CacheAppendArgs), packer(CacheAttendArgs)
 _INT_MAX = 2 ** 31 - 1
 
 
@@ -77,7 +78,7 @@ class PagedCache:
         self._error = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
         self._cache = Cache(k_pages.data_ptr(), v_pages.data_ptr(), pages, self.num_kv_heads, self.page_size,
                             self.head_dim, _dtype_code(self.dtype), self._error.data_ptr())
-        self._ref = ctypes.byref(self._cache)
+        self._ref = bytes(self._cache)
         self._device = k_pages.device
 
     def _rows(self, t, name, T=None, heads=None):
@@ -88,16 +89,16 @@ class PagedCache:
                              f"{self.head_dim}], got {tuple(t.shape)}")
         return strides
 
-    def _batch(self, T, seq_lens, block_table, cu_tokens) -> CacheBatch:
+    def _batch(self, T, seq_lens, block_table, cu_tokens) -> bytes:
         B = seq_lens.shape[0]
         if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1:
             raise ValueError(f"block_table must be [{B}, max_pages], got {tuple(block_table.shape)}")
         if cu_tokens is None and (T or B) and (B == 0 or T % B):
             raise ValueError(f"{T} rows cannot be shared by {B} sequences; pass cu_tokens")
         device = self._device
-        return CacheBatch(B, T, check_index(block_table, "block_table", device, block_table.shape),
-                          block_table.shape[1], check_index(seq_lens, "seq_lens", device, (B,)),
-                          check_index(cu_tokens, "cu_tokens", device, (B + 1,)))
+        return _pack_batch(B, T, check_index(block_table, "block_table", device, block_table.shape),
+                           block_table.shape[1], check_index(seq_lens, "seq_lens", device, (B,)),
+                           check_index(cu_tokens, "cu_tokens", device, (B + 1,)))
 
     def append(self, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor, *,
                q: Optional[torch.Tensor] = None, cu_tokens: Optional[torch.Tensor] = None,
@@ -120,7 +121,7 @@ class PagedCache:
         vs = self._rows(v, "v", T, self.num_kv_heads)
         if rotary is not None and rotary.head_dim != self.head_dim:
             raise ValueError(f"the rotation is for head_dim {rotary.head_dim}, the cache's is {self.head_dim}")
-        Hq, qs, os, q_ptr, qo_ptr = 0, (0, 0), (0, 0), None, None
+        Hq, qs, os, q_ptr, qo_ptr = 0, (0, 0), (0, 0), 0, 0
         if q is None:
             q_out = None
         else:
@@ -133,11 +134,11 @@ class PagedCache:
                 os = self._rows(q_out, "q_out", T, Hq)
             q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
         batch = self._batch(T, seq_lens, block_table, cu_tokens)
-        a = CacheAppendArgs(
+        a = _pack_append(
             Hq, q_ptr, k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qo_ptr, os[0], os[1],
-            _NO_ROTATION if rotary is None else rotary.struct,
-            head_norm(norm_eps, q_weight, k_weight, self.head_dim, self._device))
-        st = self._lib.swa_cache_append(self._ref, ctypes.byref(batch), ctypes.byref(a), current_stream(self.k_pages))
+            *(NO_ROTATION if rotary is None else rotary.fields),
+            *head_norm(norm_eps, q_weight, k_weight, self.head_dim, self._device))
+        st = self._lib.swa_cache_append(self._ref, batch, a, current_stream(self.k_pages))
         if st != 0:
             raise SwaError(st, "swa_cache_append")
         return q_out
@@ -186,14 +187,14 @@ class PagedCache:
         elif lse.dtype != torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous() or \
                 lse.device != self._device:
             raise ValueError(f"lse must be a contiguous fp32 [{T}, {Hq}] on {self._device}")
-        a = CacheAttendArgs(Hq, q.data_ptr(), qs[0], qs[1], max_tokens, max_len, window,
-                            softcap, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), None, 0)
-        refs = self._ref, ctypes.byref(batch), ctypes.byref(a)
-        need = self._lib.swa_cache_attend_workspace_bytes(*refs)
+        fields = (Hq, q.data_ptr(), qs[0], qs[1], max_tokens, max_len, window, softcap, scale, out.data_ptr(),
+                  0 if lse is None else lse.data_ptr())
+        a = _pack_attend(*fields, 0, 0)
+        need = self._lib.swa_cache_attend_workspace_bytes(self._ref, batch, a)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=self._device)
-            a.workspace, a.workspace_bytes = ws.data_ptr(), need
-        st = self._lib.swa_cache_attend(*refs, current_stream(self.k_pages))
+            a = _pack_attend(*fields, ws.data_ptr(), need)
+        st = self._lib.swa_cache_attend(self._ref, batch, a, current_stream(self.k_pages))
         if st != 0:
             raise SwaError(st, "swa_cache_attend")
         return out, lse

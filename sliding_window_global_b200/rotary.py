@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional
 
 import torch
@@ -58,15 +59,36 @@ class RotaryBackwardArgs(ctypes.Structure):
     ]
 
 
-NO_STRIDES = (0, 0, 0)
-_NO_ROTATION = Rotation(0, 0, None, 1.0)
-_NO_NORM = HeadNorm(0, 0.0, None, None, 0)
-
 # A call of a few microseconds on the GPU is bound by what the host does for it, so the
-# paths below take the cheapest spelling of each step: outputs by empty_like, the stream's
-# handle without a Stream object, and a device or stream context only where it changes
-# something.
+# paths below take the cheapest spelling of each step: argument structs packed in one go,
+# outputs by empty_like, the stream's handle without a Stream object, and a device or stream
+# context only where it changes something.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def packer(cls):
+    """A function that packs the (flattened) field values of a ctypes structure into its
+    bytes; pointers are addresses, 0 for NULL."""
+    codes = {I: "i", I64: "q", P: "Q", F: "f", ctypes.c_size_t: "Q"}
+
+    def layout(c):
+        fmt, at = "", 0
+        for name, kind in c._fields_:
+            offset = getattr(c, name).offset
+            fmt += "x" * (offset - at)
+            fmt += layout(kind) if issubclass(kind, ctypes.Structure) else codes[kind]
+            at = offset + ctypes.sizeof(kind)
+        return fmt + "x" * (ctypes.sizeof(c) - at)
+
+    s = struct.Struct("=" + layout(cls))
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_forward, _pack_backward = packer(RotaryArgs), packer(RotaryBackwardArgs)
+NO_STRIDES = (0, 0, 0)
+NO_ROTATION = (0, 0, 0, 1.0)               # fields of Rotation, of HeadNorm
+_NO_NORM = (0, 0.0, 0, 0, 0)
 
 
 def elsewhere(t: torch.Tensor, name: str, stream):
@@ -103,9 +125,9 @@ def check_rows(t: torch.Tensor, name: str, device, dims: int, dtype=None):
 
 
 def check_index(t: Optional[torch.Tensor], name: str, device, shape):
-    """An int32 tensor of the given shape (or None); returns its address."""
+    """An int32 tensor of the given shape (or None); returns its address (or 0)."""
     if t is None:
-        return None
+        return 0
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != torch.int32:
@@ -117,8 +139,8 @@ def check_index(t: Optional[torch.Tensor], name: str, device, shape):
     return t.data_ptr()
 
 
-def head_norm(norm_eps, q_weight, k_weight, head_dim: int, device) -> HeadNorm:
-    """swa_head_norm of the arguments (norm_eps None: no norm)."""
+def head_norm(norm_eps, q_weight, k_weight, head_dim: int, device):
+    """Fields of swa_head_norm (norm_eps None: no norm)."""
     if norm_eps is None:
         if q_weight is not None or k_weight is not None:
             raise ValueError("norm weights need norm_eps")
@@ -126,7 +148,7 @@ def head_norm(norm_eps, q_weight, k_weight, head_dim: int, device) -> HeadNorm:
     code, ptrs = 0, []
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is None:
-            ptrs.append(None)
+            ptrs.append(0)
             continue
         check_rows(w, name, device, 1)
         if w.shape[0] != head_dim:
@@ -135,7 +157,7 @@ def head_norm(norm_eps, q_weight, k_weight, head_dim: int, device) -> HeadNorm:
         code = _dtype_code(w.dtype)
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise TypeError("q_weight and k_weight must have one dtype")
-    return HeadNorm(1, norm_eps, ptrs[0], ptrs[1], code)
+    return 1, norm_eps, ptrs[0], ptrs[1], code
 
 
 def check_start(start: int):
@@ -203,7 +225,7 @@ class Rotary:
         if len(freq) != self.rotary_dim // 2 or not all(math.isfinite(f) for f in freq):
             raise ValueError(f"frequencies needs {self.rotary_dim // 2} finite values")
         self._freq = (ctypes.c_double * max(1, len(freq)))(*freq)
-        self.struct = Rotation(self.rotary_dim, int(self.interleaved), ctypes.addressof(self._freq), self.amplitude)
+        self.fields = (self.rotary_dim, int(self.interleaved), ctypes.addressof(self._freq), self.amplitude)
 
     def forward(self, q: torch.Tensor, k: Optional[torch.Tensor] = None, *, positions: Optional[torch.Tensor] = None,
                 start: int = 0, norm_eps: Optional[float] = None, q_weight: Optional[torch.Tensor] = None,
@@ -239,7 +261,7 @@ class Rotary:
             os = (Hq * n * D, n * D, D)
         else:
             os = self._check_out(q_out, "q_out", q)
-        kos, k_ptr, ko_ptr = NO_STRIDES, None, None
+        kos, k_ptr, ko_ptr = NO_STRIDES, 0, 0
         if k is None:
             k_out = None
         else:
@@ -249,12 +271,12 @@ class Rotary:
             else:
                 kos = self._check_out(k_out, "k_out", k)
             k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
-        a = RotaryArgs(
+        a = _pack_forward(
             B, n, Hq, Hkv, D, code, q.data_ptr(), k_ptr, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
             check_index(positions, "positions", device, (B, n)), start, q_out.data_ptr(), ko_ptr,
-            os[0], os[1], os[2], kos[0], kos[1], kos[2], self.struct,
-            head_norm(norm_eps, q_weight, k_weight, D, device))
-        st = self._lib.swa_rotary_forward(ctypes.byref(a), current_stream(q))
+            os[0], os[1], os[2], kos[0], kos[1], kos[2], *self.fields,
+            *head_norm(norm_eps, q_weight, k_weight, D, device))
+        st = self._lib.swa_rotary_forward(a, current_stream(q))
         if st != 0:
             raise SwaError(st, "swa_rotary_forward")
         return q_out, k_out
@@ -307,7 +329,7 @@ class Rotary:
             os = dq.stride()
         else:
             os = self._check_out(dq, "dq", dq_out, None)
-        oks, gk_ptr, dk_ptr = NO_STRIDES, None, None
+        oks, gk_ptr, dk_ptr = NO_STRIDES, 0, 0
         if dk_out is None:
             dk = None
         else:
@@ -322,19 +344,18 @@ class Rotary:
             dqw = torch.empty_like(q_weight, dtype=torch.float32)
         if k_weight is not None and Hkv > 0:
             dkw = torch.empty_like(k_weight, dtype=torch.float32)
-        a = RotaryBackwardArgs(
+        fields = (
             B, n, Hq, Hkv, D, _dtype_code(x_dtype), _dtype_code(dq_out.dtype), _dtype_code(dq.dtype),
-            None if q is None else q.data_ptr(), None if k is None else k.data_ptr(), qs[0], qs[1], qs[2],
+            0 if q is None else q.data_ptr(), 0 if k is None else k.data_ptr(), qs[0], qs[1], qs[2],
             ks[0], ks[1], ks[2], check_index(positions, "positions", device, (B, n)), start, dq_out.data_ptr(), gk_ptr,
             gs[0], gs[1], gs[2], gks[0], gks[1], gks[2], dq.data_ptr(), dk_ptr, os[0], os[1], os[2], oks[0], oks[1],
-            oks[2], None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(), self.struct, hn,
-            None, 0)
-        ref = ctypes.byref(a)
+            oks[2], 0 if dqw is None else dqw.data_ptr(), 0 if dkw is None else dkw.data_ptr(), *self.fields, *hn)
+        ws, need = 0, 0
         if dqw is not None or dkw is not None:
-            need = self._lib.swa_rotary_workspace_bytes(ref)
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
-            a.workspace, a.workspace_bytes = ws.data_ptr(), need
-        st = self._lib.swa_rotary_backward(ref, current_stream(dq_out))
+            need = self._lib.swa_rotary_workspace_bytes(_pack_backward(*fields, 0, 0))
+            space = torch.empty(need, dtype=torch.uint8, device=device)
+            ws = space.data_ptr()
+        st = self._lib.swa_rotary_backward(_pack_backward(*fields, ws, need), current_stream(dq_out))
         if st != 0:
             raise SwaError(st, "swa_rotary_backward")
         return (dq, dk) if norm_eps is None else (dq, dk, dqw, dkw)
