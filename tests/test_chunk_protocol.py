@@ -191,12 +191,13 @@ def simulate(pieces, rng, mistake=None):
 
     agents = [producer(), cleaner(), issuer()] + [softmax(x, t) for x in range(2) for t in range(THREADS)]
     idle = 0
+    slow = rng.choice((0.02, 0.1, 0.3)), rng.choice((0.02, 0.1, 0.3))      # how fast loads and products end
     while agents or loads or products:
         before = sum(b.arrivals + b.done * 1000 for b in bars.values()) + len(loads) + len(products) + len(agents)
         pick = rng.random()
-        if loads and pick < 0.3:
+        if loads and pick < slow[0]:
             loads.pop(rng.randrange(len(loads)))()
-        elif products and pick < 0.6:
+        elif products and pick < slow[0] + slow[1]:
             kind, what = products.pop(0)
             what() if kind == "mma" else what.arrive()
         elif agents:
