@@ -20,6 +20,8 @@ namespace {
 
 constexpr int kKeys = 64;                  // keys of a step of the CUDA-core kernel
 constexpr int kCoreThreads = 256;
+constexpr int kRowsMost = 32;              // rows of a sequence and KV head up to which the few-row kernel runs
+constexpr int kRowsWarps = 4, kRowsBlocks = 3;                      // warps of its blocks, blocks an SM
 
 template <int D, int RT>
 constexpr int core_smem_bytes() {
@@ -41,10 +43,9 @@ __device__ __forceinline__ void copy_wait() {
 // outputs (two products an instruction; reads of shared memory bound it, which more rows a
 // thread make fewer).  K of a step is fetched while V of the step before is used, and V
 // while K is, both with cp.async; where each key lies is looked up a step ahead, by one
-// thread a key.  The tile is the smallest of 16, 64 and 128 rows that the rows of a sequence
-// fill: 2 x 256 tokens of 40 heads, 8 KV heads, over 4096 keys, D = 128, take 1.40 ms with 128
-// (30 TFLOP/s) and 1.78 ms with 64 rows; one token of 8 sequences of 4000 keys 218 us with 16
-// and 370 us with 64.
+// thread a key.  The tile is 64 rows where those of a sequence fit, else 128: 2 x 256 tokens of 40
+// heads, 8 KV heads, over 4096 keys, D = 128, take 1.40 ms with 128 (30 TFLOP/s) and 1.78 ms
+// with 64 rows.
 template <int D, int RT>
 __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_constant__ CacheAttendParams p,
                                                                   int row_tiles) {
@@ -246,6 +247,256 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
   }
 }
 
+template <int D>
+constexpr int kRowsStages = 256 / D;       // steps of a warp's ring: 16 KB
+
+// Few rows (single tokens) in fp32, RT at a time: the keys' bytes bound it, so a warp works on
+// its own and keeps copies of the next step in flight. Sixteen lanes hold a key, each D/16 of its
+// elements, and a warp takes eight keys a step (two halves of four). A lane reads only what
+// it copied itself, so its own cp.async wait is all the order there is. RT x 4 partial dot
+// products a lane are summed over the lanes by halving the list at each exchange, which
+// leaves every lane RT/4 scores of its own to mask and exponentiate; the weights then go
+// back to all lanes for the V products. A block's warps take its steps in turn and are
+// joined through shared memory. Tiles of 4 or of 8 rows: more would not fit the registers.
+// 8 sequences of 4000 keys, 32/8 heads, D = 128: 53 us (5.0 TB/s; 59 with K and V loaded into
+// registers, 218 with cache_core_kernel); 32 ragged ones up to 16000 keys 272 us (86% of the
+// copy rate). Two blocks of three stages take 51 and 328 us, one of eight warps 59 and 294.
+// More rows read the keys anew a tile, from L2: 4 tokens (16 rows) of the first case 121 us, 8 tokens
+// 198 us, where cache_core_kernel takes 219 and 371.
+template <int D, int RT>
+__global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks)
+cache_rows_kernel(const __grid_constant__ CacheAttendParams p, int row_tiles) {
+  constexpr int U = 4, kStepKeys = 2 * U;  // keys of a half warp and of a step, which divide every page
+  constexpr int E = D / 16, F4 = E / 4;    // elements of a lane, in float4s 64 elements apart
+  constexpr int NL = U * RT / 16;          // scores a lane keeps: key lane / LR, rows (lane % LR) NL + i
+  constexpr int LR = 16 / U;
+  constexpr int kWarps = kRowsWarps, kThreads = kWarps * 32;
+  constexpr int NST = kRowsStages<D>;
+  __shared__ __align__(16) float sQ[RT * D];
+  extern __shared__ float smem[];          // rings of the warps, afterwards their outputs
+  __shared__ float sM[kWarps][RT], sL[kWarps][RT];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 15, half = lane >> 4;
+  const int hk = blockIdx.y;
+  const int split = blockIdx.x % p.nsplit;
+  const int rt = blockIdx.x / p.nsplit % row_tiles;
+  const int b = blockIdx.x / p.nsplit / row_tiles;
+  grid_launch_dependents();
+  const CacheSeq s = cache_seq(p, b);
+  if (s.bad && tid == 0 && rt == 0 && split == 0 && hk == 0) atomicOr(p.err, kDevErrCheck);
+  const int rows = s.count * p.G;
+  const int r0 = rt * RT;
+  if (r0 >= rows) return;
+
+  const int lo = key_begin(p, s, r0 / p.G), hi = key_end(s, min((r0 + RT - 1) / p.G, s.count - 1));
+  const int base = lo / kStepKeys * kStepKeys;
+  const int steps = hi > lo ? (hi - base + kStepKeys - 1) / kStepKeys : 0;
+  const int j0 = (int)((long long)steps * split / p.nsplit), j1 = (int)((long long)steps * (split + 1) / p.nsplit);
+
+  int klo[NL], khi[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int r = r0 + (lane % LR) * NL + i;
+    klo[i] = r < rows ? key_begin(p, s, r / p.G) : 0;
+    khi[i] = r < rows ? key_end(s, r / p.G) : 0;
+  }
+  float m[NL], l[NL], o[RT][E];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[r][e] = 0.f;
+
+  // a step's keys lie in one page: where they begin for this lane, < 0 if it does not exist
+  const int32_t* table = p.block_table + (long long)b * p.max_pages;
+  auto look_up = [&](int j) -> long long {
+    if (j >= j1) return -1;
+    const int pos = base + j * kStepKeys;
+    const int page = __ldg(table + pos / p.page_size);
+    if (page < 0 || page >= p.num_pages) {
+      if (lane == 0) atomicOr(p.err, kDevErrCheck);
+      return -1;
+    }
+    return (((long long)page * p.Hkv + hk) * p.page_size + pos % p.page_size + half * U) * D + c * 4;
+  };
+  // a lane copies what it reads itself, so that its own wait is all it needs
+  float* ring = smem + warp * NST * (2 * U * F4 * 128) + lane * 4;
+  auto fetch = [&](int slot, long long at, int j) {          // zeros for keys outside [lo, hi)
+    float* dst = ring + slot * (2 * U * F4 * 128);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int pos = base + j * kStepKeys + half * U + u;
+        const bool on = at >= 0 && pos >= lo && pos < hi;
+        const float* src = static_cast<const float*>(kv ? p.v_pages : p.k_pages) + (on ? at + u * D : 0);
+#pragma unroll
+        for (int f = 0; f < F4; ++f) copy16(dst + ((kv * U + u) * F4 + f) * 128, src + f * 64, on);
+      }
+    copy_commit();
+  };
+  uint32_t exists = 0;                     // a bit a slot
+  long long ahead;
+  {
+    long long at[NST];
+#pragma unroll
+    for (int st = 0; st < NST; ++st) at[st] = look_up(j0 + warp + st * kWarps);
+#pragma unroll
+    for (int st = 0; st < NST - 1; ++st) {
+      fetch(st, at[st], j0 + warp + st * kWarps);
+      exists |= (at[st] >= 0 ? 1u : 0u) << st;
+    }
+    ahead = at[NST - 1];
+  }
+  for (int e = tid; e < RT * (D / 4); e += kThreads) {
+    const int r = e / (D / 4), at = e % (D / 4) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + r < rows)
+      x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
+                                           (long long)(s.from + (r0 + r) / p.G) * p.q_token +
+                                           (hk * p.G + (r0 + r) % p.G) * p.q_head + at);
+    *reinterpret_cast<float4*>(sQ + r * D + at) = x;
+  }
+  __syncthreads();
+
+  int slot = 0;
+  for (int j = j0 + warp; j < j1; j += kWarps) {
+    const int refill = slot == 0 ? NST - 1 : slot - 1;
+    fetch(refill, ahead, j + (NST - 1) * kWarps);
+    exists = (exists & ~(1u << refill)) | (ahead >= 0 ? 1u : 0u) << refill;
+    ahead = look_up(j + NST * kWarps);
+    copy_wait<NST - 1>();
+    const float* now = ring + slot * (2 * U * F4 * 128);
+    float4 k4[U][F4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int f = 0; f < F4; ++f) k4[u][f] = *reinterpret_cast<const float4*>(now + (u * F4 + f) * 128);
+    float x[U * RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float4 q4[F4];
+#pragma unroll
+      for (int f = 0; f < F4; ++f) q4[f] = *reinterpret_cast<const float4*>(sQ + r * D + f * 64 + c * 4);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float even = 0.f, odd = 0.f;
+#pragma unroll
+        for (int f = 0; f < F4; ++f) {
+          ffma2(even, odd, q4[f].x, q4[f].y, k4[u][f].x, k4[u][f].y, even, odd);
+          ffma2(even, odd, q4[f].z, q4[f].w, k4[u][f].z, k4[u][f].w, even, odd);
+        }
+        x[u * RT + r] = even + odd;
+      }
+    }
+#pragma unroll
+    for (int n = U * RT / 2, bit = 8; bit > 0; n >>= 1, bit >>= 1) {
+      const bool up = lane & bit;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+        x[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+      }
+    }
+    const int pos = base + j * kStepKeys + half * U + c / LR;
+    float mx[NL], alpha[NL];
+    bool moved = false;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      x[i] *= p.scale;
+      if (p.softcap > 0.f) x[i] = p.softcap * tanhf(x[i] / p.softcap);
+      x[i] = ((exists >> slot & 1) && pos >= klo[i] && pos < khi[i]) ? x[i] : -INFINITY;
+      mx[i] = fmaxf(x[i], m[i]);
+#pragma unroll
+      for (int w = LR; w < 32; w <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], w));
+      moved = moved || mx[i] != m[i];
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        alpha[i] = m[i] == -INFINITY ? 0.f : expf(m[i] - mx[i]);
+        m[i] = mx[i];
+        l[i] *= alpha[i];
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float f = __shfl_sync(0xffffffffu, alpha[r % NL], r / NL);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[r][e] *= f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      x[i] = expf(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
+      l[i] += x[i];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float4 v4[F4];
+#pragma unroll
+      for (int f = 0; f < F4; ++f) v4[f] = *reinterpret_cast<const float4*>(now + ((U + u) * F4 + f) * 128);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float w = __shfl_sync(0xffffffffu, x[r % NL], half * 16 + u * LR + r / NL);
+#pragma unroll
+        for (int f = 0; f < F4; ++f) {
+          ffma2(o[r][4 * f], o[r][4 * f + 1], w, w, v4[f].x, v4[f].y, o[r][4 * f], o[r][4 * f + 1]);
+          ffma2(o[r][4 * f + 2], o[r][4 * f + 3], w, w, v4[f].z, v4[f].w, o[r][4 * f + 2], o[r][4 * f + 3]);
+        }
+      }
+    }
+    slot = slot == NST - 1 ? 0 : slot + 1;
+  }
+  copy_wait<0>();
+  __syncthreads();                         // the rings are read
+
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+#pragma unroll
+    for (int w = LR; w < 32; w <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+    if (lane < LR) {
+      sM[warp][lane * NL + i] = m[i];
+      sL[warp][lane * NL + i] = l[i];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      o[r][e] += __shfl_xor_sync(0xffffffffu, o[r][e], 16);
+      if (half == 0) smem[(warp * RT + r) * D + e / 4 * 64 + c * 4 + e % 4] = o[r][e];
+    }
+  __syncthreads();
+  for (int e = tid; e < RT * D; e += kThreads) {
+    const int r = e / D, d = e % D;
+    if (r0 + r >= rows) break;
+    float top = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sM[w][r]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = sM[w][r] == -INFINITY ? 0.f : expf(sM[w][r] - top);
+      sum += f * sL[w][r];
+      acc += f * smem[(w * RT + r) * D + d];
+    }
+    const bool has = top != -INFINITY;
+    const float value = has ? acc / sum : 0.f, lse = has ? top + logf(sum) : -INFINITY;
+    const long long row = (long long)(s.from + (r0 + r) / p.G) * p.Hq + hk * p.G + (r0 + r) % p.G;
+    if (p.nsplit > 1) {
+      const long long pr = (long long)split * p.T * p.Hq + row;
+      p.part_o[pr * D + d] = value;
+      if (d == 0) p.part_lse[pr] = lse;
+    } else {
+      static_cast<float*>(p.out)[row * D + d] = value;
+      if (p.lse && d == 0) p.lse[row] = lse;
+    }
+  }
+}
+
 // out = sum_s exp(lse_s - lse) out_s over the splits in order, lse = log sum_s exp(lse_s):
 // one warp a row.
 template <int D>
@@ -253,6 +504,7 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  grid_dependency_wait();
   const int h = (int)(id % p.Hq);
   const int i = (int)(id / p.Hq % p.max_tokens);
   const long long b = id / p.Hq / p.max_tokens;
@@ -261,17 +513,23 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
   if (i >= s.count) return;
   const long long row = (long long)(s.from + i) * p.Hq + h, step = (long long)p.T * p.Hq;
   float top = -INFINITY;
-  for (int k = 0; k < p.nsplit; ++k) top = fmaxf(top, p.part_lse[k * step + row]);
+  for (int k = lane; k < p.nsplit; k += 32) top = fmaxf(top, p.part_lse[k * step + row]);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
   float acc[E], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int k = 0; k < p.nsplit; ++k) {
-    const float w = p.part_lse[k * step + row];
-    if (w == -INFINITY) continue;          // a split without keys (NaN goes on)
-    const float f = expf(w - top);
-    sum += f;
+  for (int k0 = 0; k0 < p.nsplit; k0 += 32) {
+    const float w = k0 + lane < p.nsplit ? p.part_lse[(k0 + lane) * step + row] : -INFINITY;
+    const float mine = w == -INFINITY ? 0.f : expf(w - top);   // a split without keys has zeros (NaN goes on)
+    const int n = min(32, p.nsplit - k0);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float f = __shfl_sync(0xffffffffu, mine, k);
+      sum += f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += f * p.part_o[(k * step + row) * D + lane * E + e];
+      for (int e = 0; e < E; ++e) acc[e] += f * p.part_o[((k0 + k) * step + row) * D + lane * E + e];
+    }
   }
   const bool has = sum != 0.f;
   const float inv = has ? 1.f / sum : 0.f;
@@ -292,18 +550,37 @@ cudaError_t launch_core(const CacheAttendParams& p, int row_tiles, cudaStream_t 
   return cudaGetLastError();
 }
 
+template <int D, int RT>
+cudaError_t launch_rows(const CacheAttendParams& p, int row_tiles, cudaStream_t s) {
+  constexpr int ring = kRowsWarps * kRowsStages<D> * 16 * D * 4, out = kRowsWarps * RT * D * 4;
+  constexpr int smem = ring > out ? ring : out;
+  static_assert(kRowsBlocks * (smem + RT * D * 4 + 8 * kRowsWarps * RT + 1024) <= 228 * 1024, "blocks an SM");
+  const cudaError_t e = allow_smem<&cache_rows_kernel<D, RT>>(smem);
+  if (e != cudaSuccess) return e;
+  cache_rows_kernel<D, RT><<<dim3((unsigned)((long long)p.B * row_tiles * p.nsplit), p.Hkv), kRowsWarps * 32, smem, s>>>(
+      p, row_tiles);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch_core(const CacheAttendParams& p, int tile_rows, int row_tiles, cudaStream_t s) {
-  return tile_rows == 16 ? launch_core<D, 1>(p, row_tiles, s)
+  return tile_rows == 4 ? launch_rows<D, 4>(p, row_tiles, s)
+         : tile_rows == 8 ? launch_rows<D, 8>(p, row_tiles, s)
          : tile_rows == 64 ? launch_core<D, 4>(p, row_tiles, s) : launch_core<D, 8>(p, row_tiles, s);
 }
 
 cudaError_t launch_merge(const CacheAttendParams& p, cudaStream_t s) {
   const long long rows = (long long)p.B * p.max_tokens * p.Hq;
-  const unsigned blocks = (unsigned)((rows + 3) / 4);
-  if (p.D == 64) cache_merge_kernel<64><<<blocks, 128, 0, s>>>(p);
-  else cache_merge_kernel<128><<<blocks, 128, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.D == 64 ? cache_merge_kernel<64> : cache_merge_kernel<128>, p);
 }
 
 // How a call is cut up, from sizes only: which kernel, and its parts.
@@ -336,12 +613,30 @@ AttendSplit attend_split(const swa_cache& c, const swa_cache_batch& b, const swa
   }
   r.kernel = AttendSplit::kCore;
   const long long rows = (long long)max_tokens * G;
-  r.tile_rows = rows <= 16 ? 16 : rows <= 64 ? 64 : 128;
+  r.tile_rows = rows <= 4 ? 4 : rows <= kRowsMost ? 8 : rows <= 64 ? 64 : 128;
   r.row_tiles = (int)((rows + r.tile_rows - 1) / r.tile_rows);
-  // parts of a step of keys at least, two blocks an SM
-  const long long blocks = (long long)b.batch * r.row_tiles * c.num_kv_heads;
-  const long long want = (148 * 2 + blocks - 1) / std::max<long long>(blocks, 1);
-  r.nsplit = (int)std::max<long long>(1, std::min<long long>({want, reach / kKeys, 64}));
+  const long long blocks = std::max<long long>(1, (long long)b.batch * r.row_tiles * c.num_kv_heads);
+  if (r.tile_rows > 8) {
+    // parts of a step of keys at least, two blocks an SM
+    r.nsplit = (int)std::max<long long>(1, std::min<long long>({(148 * 2 + blocks - 1) / blocks, reach / kKeys, 64}));
+  } else {
+    // One wave of blocks, in parts of 128 keys (four steps a warp) at least. Several sequences may
+    // differ in length, so up to four waves in parts of 512 keys where these fill the GPU better
+    // than 80%: 32 ragged sequences of up to 16000 keys 476 us in one wave, 328 in four (two
+    // blocks an SM).
+    const long long slots = 148 * kRowsBlocks;
+    const auto fill = [&](long long n) { return (double)(n * blocks) / ((n * blocks + slots - 1) / slots * slots); };
+    long long n = std::max<long long>(1, std::min(reach / 128, slots / blocks));
+    double best = std::min(fill(n), 0.8);
+    for (int waves = 2; waves <= 4 && b.batch > 1; ++waves) {
+      const long long m = std::min(reach / 512, slots * waves / blocks);
+      if (m > n && fill(m) > best * 1.03) {
+        best = fill(m);
+        n = m;
+      }
+    }
+    r.nsplit = (int)n;
+  }
   if (r.nsplit > 1) r.bytes = (size_t)r.nsplit * b.num_tokens * a.num_q_heads * (c.head_dim + 1) * 4;
   return r;
 }

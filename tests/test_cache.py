@@ -319,6 +319,14 @@ ATTENDS = [
     ("heads_128", BF16, 128, 1, 64, 32, None, 0.0, [3], [77]),
     ("fp32_tokens", FP32, 12, 12, 64, 16, None, 0.0, [1, 1], [300, 7]),
     ("fp32_long", FP32, 4, 1, 128, 64, None, 30.0, [2], [3000]),
+    ("fp32_group", FP32, 32, 8, 128, 64, None, 0.0, [1] * 6, [1, 7, 8, 9, 64, 2900]),
+    ("fp32_window", FP32, 7, 1, 64, 16, 130, 0.0, [1] * 4, [5, 131, 132, 1003]),
+    ("fp32_guesses", FP32, 6, 2, 128, 48, 33, 0.0, [5, 1, 0, 3], [5, 20, 9, 517]),
+    ("fp32_guesses_cap", FP32, 10, 2, 64, 32, None, 5.0, [6, 2], [70, 700]),
+    ("fp32_rows_32", FP32, 8, 1, 128, 16, None, 0.0, [4, 4], [4, 333]),
+    ("fp32_rows_33", FP32, 11, 1, 64, 16, None, 0.0, [3, 3], [3, 333]),
+    ("fp32_many_parts", FP32, 2, 1, 64, 128, None, 0.0, [1], [9001]),
+    ("fp32_waves", FP32, 4, 4, 128, 16, 2500, 0.0, [1] * 30, [1 + 977 * i % 2999 for i in range(30)]),
     ("fp32_chunk", FP32, 6, 2, 64, 48, 50, 0.0, [100, 1, 0, 13], [170, 3, 9, 13]),
 ]
 
@@ -356,7 +364,8 @@ def test_attend(case):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype,new,G", [(BF16, [1, 1], 4), (BF16, [40, 3], 4), (FP32, [40, 3], 2), (BF16, [6, 5], 8)])
+@pytest.mark.parametrize("dtype,new,G", [(BF16, [1, 1], 4), (BF16, [40, 3], 4), (FP32, [40, 3], 2), (BF16, [6, 5], 8),
+                                         (FP32, [1, 1], 4), (FP32, [6, 5], 4)])
 def test_pages_that_do_not_exist_are_left_out(dtype, new, G):
     s = _problem(dtype, 2, 128, 16, new, [100, 50], 13)
     s["table"][0, 2] = -5                                   # keys 32-47
@@ -416,7 +425,7 @@ def test_broken_bounds_stay_in_bounds(new):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype,T,G", [(BF16, 6, 4), (BF16, 140, 4), (FP32, 20, 1)])
+@pytest.mark.parametrize("dtype,T,G", [(BF16, 6, 4), (BF16, 140, 4), (FP32, 20, 1), (FP32, 60, 1)])
 def test_sequences_that_claim_the_same_rows(dtype, T, G):
     """cu_tokens that go back to 0 name more rows than there are: in bounds, and reported."""
     s = _problem(dtype, 2, 64, 16, [T, 0, T], [200, 10, 160], 37)
