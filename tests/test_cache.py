@@ -381,6 +381,22 @@ def test_pages_that_do_not_exist_are_left_out(dtype, new, G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,new,G", [(BF16, 1, 4), (BF16, 70, 2), (FP32, 1, 4), (FP32, 40, 2)])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("at", [3, 30])
+def test_a_nan_among_the_keys_is_not_lost(dtype, new, G, cap, at):
+    s = _problem(dtype, 2, 128, 16, [new, new], [120, 90], 17)
+    page, slot = int(s["table"][0, at // 16]), at % 16
+    s["k"][page, 0, slot, 5] = math.nan                     # sequence 0, KV head 0
+    q = torch.randn((s["total"], 2 * G, 128), generator=s["g"]).to(dtype).cuda()
+    out, lse = s["cache"].attend(q, s["lens"].cuda(), s["table"].cuda(), cu_tokens=s["cu"].cuda(), max_tokens=new,
+                                 softcap=cap)
+    assert bool(out[:new, :G].isnan().all()) and bool(lse[:new, :G].isnan().all())
+    assert bool(out[:new, G:].isfinite().all()) and bool(out[new:].isfinite().all())
+    assert s["cache"].check() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("new", [[2, 2], [70, 70]])
 def test_broken_bounds_stay_in_bounds(new):
     """Lengths and tokens beyond what the call states, negative lengths, cu_tokens that
