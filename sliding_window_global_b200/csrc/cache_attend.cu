@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kCoreThreads) cache_core_kernel(const __grid_c
     const int r = r0 + ty * RT + i;
     if (r >= rows) continue;
     const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
-    const bool has = m[i] != -INFINITY;
+    const bool has = l[i] != 0.f;          // also where every score is NaN
     const float inv = has ? 1.f / l[i] : 0.f;
     const float lse = has ? m[i] + logf(l[i]) : -INFINITY;
     if (p.nsplit > 1) {
@@ -479,11 +479,11 @@ cache_rows_kernel(const __grid_constant__ CacheAttendParams p, int row_tiles) {
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sM[w][r]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = sM[w][r] == -INFINITY ? 0.f : expf(sM[w][r] - top);
+      const float f = sL[w][r] == 0.f ? 0.f : expf(sM[w][r] - top);
       sum += f * sL[w][r];
       acc += f * smem[(w * RT + r) * D + d];
     }
-    const bool has = top != -INFINITY;
+    const bool has = sum != 0.f;           // also where every score is NaN
     const float value = has ? acc / sum : 0.f, lse = has ? top + logf(sum) : -INFINITY;
     const long long row = (long long)(s.from + (r0 + r) / p.G) * p.Hq + hk * p.G + (r0 + r) % p.G;
     if (p.nsplit > 1) {

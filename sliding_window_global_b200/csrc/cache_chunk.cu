@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       if (!mbar_wait_bounded(&o_full[x], oc & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
       ++oc;
       tc_fence_after();
-      const bool has = m != -INFINITY;
+      const bool has = l != 0.f;           // also where every score is NaN
       const float inv = has ? 1.f / l : 0.f;
       const float lse = has ? (m + __log2f(l)) * kLn2 : -INFINITY;
       // Rows leave through shared memory, so that eight lanes write 128 bytes of a row: 64 bf16

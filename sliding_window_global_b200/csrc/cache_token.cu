@@ -206,7 +206,7 @@ __device__ __forceinline__ void join_unit(const CacheAttendParams& p, const Cach
   };
   constexpr int Q = D / 4;                             // 16-byte pieces of a row
   auto store = [&](int r, int c, float4 acc) {
-    const bool has = sTop[r] != -INFINITY;
+    const bool has = sSum[r] != 0.f;       // also where every score is NaN
     const float inv = has ? 1.f / sSum[r] : 0.f;
     const long long row = (long long)(s.from + r / p.G) * p.Hq + hk * p.G + r % p.G;
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * D + c) =
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int r = mt * 16 + (lane >> 2) + 8 * x;
         if (r >= rows) continue;
-        const bool has = m[mt][x] != -INFINITY;
+        const bool has = sum != 0.f;       // also where every score is NaN
         const float inv = has ? 1.f / sum : 0.f;
         const float lse = has ? (m[mt][x] + log2f(sum)) * kLn2 : -INFINITY;
         if (whole) {

@@ -397,6 +397,25 @@ def test_a_nan_among_the_keys_is_not_lost(dtype, new, G, cap, at):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,new,G,length", [(BF16, 1, 4, 9), (BF16, 1, 4, 9000), (BF16, 2, 12, 700), (BF16, 70, 2, 90),
+                                                (BF16, 200, 1, 5000), (FP32, 1, 4, 9), (FP32, 3, 4, 3000),
+                                                (FP32, 40, 2, 90)])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_a_nan_query_is_not_lost(dtype, new, G, length, cap):
+    """Every score of its row is NaN; the rows beside it are as without it."""
+    s = _problem(dtype, 1, 64, 16, [new], [length], 19)
+    q = torch.randn((new, G, 64), generator=s["g"]).to(dtype).cuda()
+    bad = q.clone()
+    bad[new // 2, G // 2, 7] = math.nan
+    run = lambda x: s["cache"].attend(x, s["lens"].cuda(), s["table"].cuda(), softcap=cap)
+    (out, lse), (want, want_lse) = run(bad), run(q)
+    hit = torch.zeros((new, G), dtype=torch.bool)
+    hit[new // 2, G // 2] = True
+    assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("new", [[2, 2], [70, 70]])
 def test_broken_bounds_stay_in_bounds(new):
     """Lengths and tokens beyond what the call states, negative lengths, cu_tokens that
