@@ -46,7 +46,8 @@ constexpr int kStages = 2;
 constexpr uint32_t kSub = 128 * 128;                      // 128 rows of 128 bytes, swizzled
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;                 // log2 units
-constexpr int kShortUnit = 16;                            // units of up to so many key tiles are not cut
+constexpr int kShortUnit = 16;                            // units of up to so many key tiles are not cut,
+constexpr int kShortIfFew = 6, kDirectIfFew = 12;         // where they fill half the GPU at most: see chunk_split
 constexpr int kMinPiece = 4;                              // nor is a unit cut this close to its ends
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kCapPoly = 8;                            // exponentials of 32 on the FMA pipe where scores are capped
@@ -79,6 +80,7 @@ struct ChunkParams {
   float* part_o;                   // [runs, 2, 256, D]
   float* part_lse;                 // [runs, 2, 256]
   int num_runs, tile_tokens, unit_tokens, box, max_entries;
+  int short_unit;                  // units of up to so many key tiles are not cut
   int direct;                      // a block a unit, no list
   float scale_log2;
 };
@@ -189,8 +191,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
       r.entry = lo;
       r.hk = (int)(in / tiles);
       r.j = (int)(in % tiles);
-      const bool to_start = tiles <= kShortUnit ? 2 * r.j < tiles : r.j < kMinPiece;
-      const bool to_end = tiles <= kShortUnit ? !to_start : tiles - r.j < kMinPiece;
+      const bool to_start = tiles <= p.short_unit ? 2 * r.j < tiles : r.j < kMinPiece;
+      const bool to_end = tiles <= p.short_unit ? !to_start : tiles - r.j < kMinPiece;
       if (to_start) {
         r.step -= r.j;
         r.j = 0;
@@ -825,27 +827,46 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
   if (p.runs[c - 1].step > u0) return;                    // not the first cut of its unit
   const int x = r / kTile, row = r % kTile, tok = x * p.tile_tokens + row / p.a.G;
   if (row >= p.tile_tokens * p.a.G || tok >= en.tokens) return;
-  float top = -INFINITY, l = 0.f, o[E];
+  // a lane a part, 32 of them at a time: first their largest lse, then their weights
+  auto part_of = [&](int k) { return ((long long)k * 2 + (k == c - 1 ? 1 : 0)) * kUnitRows + r; };
+  auto lse_of = [&](int k, bool& more) {                  // -inf: no part, or no key in it
+    const long long step = k < p.num_runs ? p.runs[k].step : u1;
+    more = __all_sync(0xffffffffu, step < u1);
+    return step < u1 && p.runs[k + 1].step > step ? p.part_lse[part_of(k)] : -INFINITY;
+  };
+  bool more = true;
+  float top = -INFINITY, first = 0.f;
+  for (int k = c - 1; more; k += 32) {
+    const float lse = lse_of(k + lane, more);
+    if (k == c - 1) first = lse;
+    top = fmaxf(top, lse);
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+  float l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int k = c - 1; k < p.num_runs && p.runs[k].step < u1; ++k) {
-    if (p.runs[k].step == p.runs[k + 1].step) continue;  // an empty run
-    const long long part = ((long long)k * 2 + (k == c - 1 ? 1 : 0)) * kUnitRows + r;
-    const float lse = p.part_lse[part];
-    if (lse == -INFINITY) continue;                      // no key in this part (a NaN goes on)
-    float x[E];
+  more = true;
+  for (int k0 = c - 1; more; k0 += 32) {
+    float lse = first;
+    if (k0 == c - 1) more = __all_sync(0xffffffffu, k0 + lane < p.num_runs && p.runs[min(k0 + lane, p.num_runs)].step < u1);
+    else lse = lse_of(k0 + lane, more);
+    const float mine = lse == -INFINITY ? 0.f : ex2_approx((lse - top) * kLog2e);      // a NaN goes on
+    const uint32_t parts = __ballot_sync(0xffffffffu, lse != -INFINITY);
+    const int n = 32 - __clz(parts);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float f = __shfl_sync(0xffffffffu, mine, k);
+      const bool on = parts >> k & 1;                    // else nothing was written there
+      const float2* src = reinterpret_cast<const float2*>(p.part_o + part_of(k0 + k) * D) + lane;
+      l += f;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(p.part_o + part * D + lane * 2 + 64 * (e / 2));
-      x[e] = v.x;
-      x[e + 1] = v.y;
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = on ? src[16 * e] : make_float2(0.f, 0.f);
+        o[e] += f * v.x;
+        o[e + 1] += f * v.y;
+      }
     }
-    const float mx = fmaxf(top, lse);
-    const float keep = top == -INFINITY ? 0.f : ex2_approx((top - mx) * kLog2e), f = ex2_approx((lse - mx) * kLog2e);
-    top = mx;
-    l = l * keep + f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + f * x[e];
   }
   const bool has = l != 0.f;
   const float inv = has ? 1.f / l : 0.f;
@@ -899,16 +920,22 @@ ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int m
   // Units of one query tile, a block each, where all of them fit on the GPU at once; else
   // of two, which share their keys' loads and hide each other's latencies. A block a unit
   // without a list needs units that are short and sequences that one warp can look through.
+  // Where the units leave half the GPU idle, the long ones among them are cut after all: 256
+  // tokens over 1900 keys (8/8 heads) 43 -> 27 us, 16 over 2000 (32/8) 39 -> 23, while 900
+  // over 950 (4/1, 8 tiles a unit) take 23 a block each and 29 cut.
   for (int tiles_per_unit = 1; tiles_per_unit <= 2; ++tiles_per_unit) {
     t.unit_tokens = tiles_per_unit * t.tile_tokens;
     t.max_entries = (int)(T / t.unit_tokens + std::min<long long>(B, T));
     // key tiles of a unit at most
     const long long reach = window < 0 ? max_len : std::min<long long>(max_len, (long long)window + t.unit_tokens);
     const long long tiles = (reach + t.box + kTile - 1) / kTile + 1;
-    t.split = tiles > kShortUnit;
     const long long units = (long long)t.max_entries * Hkv;
-    t.direct = !t.split && units <= 148 && B <= 1024;
-    t.runs = (int)std::min<long long>(148, t.direct ? units : std::max<long long>(1, units * tiles));
+    const bool few = units <= 74;
+    t.short_unit = few ? kShortIfFew : kShortUnit;
+    t.direct = units <= 148 && B <= 1024 && tiles <= (few ? kDirectIfFew : kShortUnit);
+    t.split = !t.direct && tiles > t.short_unit;
+    // two key tiles a run at least
+    t.runs = (int)std::min<long long>(148, t.direct ? units : std::max<long long>(1, units * tiles / 2));
     if (t.direct) break;
   }
   if (t.direct) return t;
@@ -931,6 +958,7 @@ cudaError_t launch_cache_chunk(const CacheAttendParams& a, const ChunkSplit& t, 
     return cudaErrorInvalidValue;
   p.a = a;
   p.direct = t.direct;
+  p.short_unit = t.short_unit;
   p.unit_tokens = t.unit_tokens;
   if (!t.direct) {
     char* ws = static_cast<char*>(workspace);

@@ -69,6 +69,7 @@ struct ChunkSplit {
   int runs;                         // blocks, each with an equal run of key tiles
   int tile_tokens;                  // tokens of a query tile: 128 rows / heads of a group
   int unit_tokens;                  // tokens of a unit: one query tile's or two's
+  int short_unit;                   // units of up to so many key tiles are not cut
   bool direct;                      // a block a unit, no list of work
   int box;                          // keys of one load: they lie in one page
   int max_entries;                  // units of all sequences, for one KV head

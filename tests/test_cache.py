@@ -314,6 +314,8 @@ ATTENDS = [
     ("chunk_cap", BF16, 12, 12, 64, 128, None, 20.0, [140], [290]),
     ("chunk_self", BF16, 3, 1, 128, 32, 0, 0.0, [64, 65], [64, 100]),
     ("chunk_long", BF16, 4, 1, 128, 128, None, 0.0, [260], [3001]),
+    ("chunk_few", BF16, 8, 2, 64, 32, None, 20.0, [70, 33], [1900, 1500]),
+    ("chunk_many_parts", BF16, 8, 1, 128, 64, None, 0.0, [9], [9001]),
     ("sequences_600", BF16, 2, 1, 64, 16, None, 0.0, [1] * 600, [1 + 7 * i % 41 for i in range(600)]),
     ("sequences_600_rows_40", BF16, 8, 1, 64, 16, 20, 0.0, [5] * 599 + [6], [6 + 7 * i % 41 for i in range(600)]),
     ("heads_128", BF16, 128, 1, 64, 32, None, 0.0, [3], [77]),
