@@ -22,7 +22,8 @@
 //
 // A capped score is cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), so three of its
 // operations want the MUFU instead of one: a quarter of the exponentials go to the FMA pipe there (a
-// 4096-token chunk over 16384 keys 1692 -> 1622 us; 1664 with half of them, 1821 with all).
+// 4096-token chunk over 16384 keys 1546 us; 1566 with half of them). Registers are split so that this
+// form spills none either (200 a softmax thread: 1622 us).
 //
 // Warp roles: 0-3 softmax of tile A, 4-7 of tile B, 8 loads, 9 MMAs, 10 zeroes the values at
 // positions outside the unit's keys (P is 0 there, but 0 times a NaN would not be).
@@ -39,7 +40,7 @@ namespace swa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 200, kRegsControl = 104;
+constexpr int kRegsSoftmax = 216, kRegsControl = 72;
 static_assert(256 * kRegsSoftmax + 128 * kRegsControl <= kThreads * 168 && 2 * kRegsSoftmax + kRegsControl <= 3 * 168,
               "setmaxnreg split exceeds the launch budget or a sub-partition's registers");
 constexpr int kStages = 2;
