@@ -606,7 +606,8 @@ AttendSplit attend_split(const swa_cache& c, const swa_cache_batch& b, const swa
       r.bytes = r.token.bytes;
     } else {
       r.kernel = AttendSplit::kChunk;
-      r.chunk = chunk_split(b.batch, b.num_tokens, c.num_kv_heads, G, c.head_dim, c.page_size, max_len, a.window);
+      r.chunk = chunk_split(b.batch, b.num_tokens, c.num_kv_heads, G, c.head_dim, c.page_size, max_tokens, max_len,
+                            a.window);
       r.bytes = r.chunk.bytes;
     }
     return r;

@@ -15,17 +15,19 @@
 // that a cut goes through leaves a partial result in each of its runs, joined afterwards in
 // the order of the keys; short units are never cut. Where the units are few and short enough
 // for a block each, there is no list: each block finds its own unit (of one query tile, if
-// even these are few enough).
+// even these are few enough). Sequences that fill one query tile each run two blocks an SM
+// (ONE), with one buffer of K and one of V that are freed apart, so that one block's softmax
+// runs beside the other's products: see chunk_split.
 //
 // Measured: a 4096-token chunk over 16384 keys, 32/8 heads, D = 128, 804 us (1.20 PFLOP/s, 73% of
-// the measured burst rate); six ragged chunks of up to 2048 tokens in a 512-key window 112-117 us.
+// the measured burst rate); six ragged chunks of up to 2048 tokens in a 512-key window 105 us.
 //
 // A capped score is cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), so three of its
 // operations want the MUFU instead of one: a quarter of the exponentials go to the FMA pipe there (a
 // 4096-token chunk over 16384 keys 1546 us; 1566 with half of them). Registers are split so that this
 // form spills none either (200 a softmax thread: 1622 us).
 //
-// Warp roles: 0-3 softmax of tile A, 4-7 of tile B, 8 loads, 9 MMAs, 10 zeroes the values at
+// Warp roles (ONE has no tile B: 4 loads and so on): 0-3 softmax of tile A, 4-7 of tile B, 8 loads, 9 MMAs, 10 zeroes the values at
 // positions outside the unit's keys (P is 0 there, but 0 times a NaN would not be).
 #include <cuda_bf16.h>
 
@@ -41,6 +43,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kRegsSoftmax = 216, kRegsControl = 72;
+constexpr int kOneThreads = 256, kOneRegsSoftmax = 192, kOneRegsControl = 64;   // units of one query tile, two blocks an SM
+static_assert(128 * (kOneRegsSoftmax + kOneRegsControl) <= kOneThreads * 128, "setmaxnreg split exceeds the launch budget");
 static_assert(256 * kRegsSoftmax + 128 * kRegsControl <= kThreads * 168 && 2 * kRegsSoftmax + kRegsControl <= 3 * 168,
               "setmaxnreg split exceeds the launch budget or a sub-partition's registers");
 constexpr int kStages = 2;
@@ -306,21 +310,32 @@ struct Walk {
   }
 };
 
-template <int D>
+struct ChunkShared {
+  ChunkEntry own;                  // direct calls: this block's unit
+  uint32_t missing[kStages];       // 16-key groups of a key tile whose page does not exist
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+
+template <int D, bool ONE>
 struct ChunkCfg {
+  static constexpr int kTiles = ONE ? 1 : 2;                // query tiles
+  static constexpr int kBuffers = ONE ? 1 : kStages;        // of K and of V
   static constexpr uint32_t kTileBytes = 128u * D * 2u;
-  static constexpr uint32_t kKOff = 2 * kTileBytes;
-  static constexpr uint32_t kVOff = kKOff + kStages * kTileBytes;
-  static constexpr uint32_t kOutOff = kVOff + kStages * kTileBytes;   // 4 KB a softmax warp: 32 rows x 64 columns
-  static constexpr uint32_t kBarOff = kOutOff + 8 * 4096;
-  static constexpr int kNumBars = 2 + 2 + 4 * kStages + 2 + 2 + 2 + 2;
-  static constexpr uint32_t kSmemBytes = kBarOff + kNumBars * 8 + 1024;
-  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kKOff = kTiles * kTileBytes;
+  static constexpr uint32_t kVOff = kKOff + kBuffers * kTileBytes;
+  static constexpr uint32_t kOutOff = kVOff + kBuffers * kTileBytes;   // 4 KB a softmax warp: 32 rows x 64 columns
+  static constexpr uint32_t kBarOff = kOutOff + kTiles * 4 * 4096;
+  static constexpr int kNumBars = 2 + 2 + 5 * kStages + 2 + 2 + 2 + 2;
+  static constexpr uint32_t kUnitOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr uint32_t kSmemBytes = kUnitOff + sizeof(ChunkShared);
+  static constexpr uint32_t kTmemCols = ONE ? 256 : 512;
   // TMEM columns: S_A | S_B | O_A | O_B, P over S
   __host__ __device__ static constexpr uint32_t s_col(int x) { return x ? 128u : 0u; }
-  __host__ __device__ static constexpr uint32_t o_col(int x) { return 256u + (x ? D : 0); }
+  __host__ __device__ static constexpr uint32_t o_col(int x) { return ONE ? 128u : 256u + (x ? D : 0); }
 };
-static_assert(ChunkCfg<128>::kSmemBytes + 64 <= 227 * 1024, "shared memory");
+static_assert(ChunkCfg<128, false>::kSmemBytes <= 227 * 1024 && 2 * (ChunkCfg<128, true>::kSmemBytes + 1024) <= 228 * 1024,
+              "shared memory");
 
 // A value that is the same in every lane, said so to the compiler.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -341,12 +356,15 @@ __device__ __forceinline__ float row_max(const float (&x)[kTile]) {
   return max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), max3(m[6], m[7], m[7]));
 }
 
-template <int D, bool CAP>
-__global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
-  using C = ChunkCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+template <int D, bool CAP, bool ONE>
+__global__ void __launch_bounds__(ONE ? kOneThreads : kThreads, ONE ? 2 : 1)
+cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
+  using C = ChunkCfg<D, ONE>;
+  constexpr int NX = C::kTiles, NB = C::kBuffers;
+  constexpr int kLoads = 4 * NX, kMma = kLoads + 1, kClear = kLoads + 2;   // warp roles behind the softmax's
+  constexpr int kInc = ONE ? kOneRegsSoftmax : kRegsSoftmax, kDec = ONE ? kOneRegsControl : kRegsControl;
+  // no static shared memory lies before it, so it begins on a 1024-byte boundary
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::kKOff;
   uint8_t* sV = smem + C::kVOff;
@@ -356,17 +374,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
   uint64_t* k_full = bars + 4;             // [kStages] K of a key tile has landed
   uint64_t* v_full = k_full + kStages;     // V has landed
   uint64_t* v_ready = v_full + kStages;    // V is free of values outside the unit's keys
-  uint64_t* kv_empty = v_ready + kStages;
-  uint64_t* s_full = kv_empty + kStages;   // [2]
+  uint64_t* kv_empty = v_ready + kStages;  // V has been used, and K with two buffers
+  uint64_t* k_empty = kv_empty + kStages;  // one buffer: K has been used
+  uint64_t* s_full = k_empty + kStages;    // [2]
   uint64_t* p_half = s_full + 2;           // [2] P of keys 0-63 written
   uint64_t* p_full = p_half + 2;           // [2]
   uint64_t* o_full = p_full + 2;           // [2]
-  __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
-  __shared__ ChunkEntry own;               // direct calls: this block's unit
-  __shared__ uint32_t missing[kStages];    // 16-key groups of a key tile whose page does not exist
+  ChunkShared& shared = *reinterpret_cast<ChunkShared*>(smem + C::kUnitOff);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) % 1024 != 0) {        // the swizzled tiles rest on it
+    if (tid == 0) atomicOr(p.a.err, kDevErrCheck);
+    return;
+  }
   if (tid == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
@@ -381,26 +401,28 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       mbar_init(&v_full[s], 1);
       mbar_init(&v_ready[s], 1);
       mbar_init(&kv_empty[s], 1);
+      mbar_init(&k_empty[s], 1);
     }
-    abort_flag = 0;
+    shared.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
-    tmem_alloc(&tmem_slot, C::kTmemCols);
+  if (warp == kMma) {
+    tmem_alloc(&shared.tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
-  if (p.direct && warp == 8) find_unit(p, lane, &own);
+  if (p.direct && warp == kLoads) find_unit(p, lane, &shared.own);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  volatile int* abort_v = &abort_flag;
+  const uint32_t tmem = shared.tmem_slot;
+  const ChunkEntry& own = shared.own;
+  volatile int* abort_v = &shared.abort_flag;
   grid_dependency_wait();                  // the list of work
   grid_launch_dependents();
 
-  if (warp == 8) {
+  if (warp == kLoads) {
     // ------------------------------------------------------------ loads
-    setmaxnreg_dec<kRegsControl>();
+    setmaxnreg_dec<kDec>();
     const int halves = D / 64, boxes = kTile / p.box;
     const int box = lane / halves, sub = lane % halves;    // of a key tile: this lane's box
     const bool loads = lane < boxes * halves;
@@ -416,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       const Half ha = half_of(p, pc, 0), hb = half_of(p, pc, 1);
       const int lo = ha.lo, hi = hb.tokens > 0 ? hb.hi : ha.hi;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < NX; ++x) {
         const Half& h = x ? hb : ha;
         if (!ok || h.e <= h.a) continue;
         if (qloads[x] > 0) ok = mbar_wait_bounded(&q_empty[x], (qloads[x] - 1) & 1, abort_v, kWaitLimitNs);
@@ -447,26 +469,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           }
         }
         miss = __reduce_or_sync(0xffffffffu, miss);
-        if (kv >= kStages) ok = mbar_wait_bounded(&kv_empty[st], (kv / kStages - 1) & 1, abort_v, kWaitLimitNs);
+        // the step whose buffers these are
+        const int from = kv - NB, fs = (from + kStages) % kStages;
+        if (from >= 0) ok = mbar_wait_bounded(ONE ? &k_empty[fs] : &kv_empty[fs], (from / kStages) & 1, abort_v, kWaitLimitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
-          missing[st] = miss;
+          shared.missing[st] = miss;
           if (miss) atomicOr(p.a.err, kDevErrCheck);
           mbar_arrive_expect_tx(&k_full[st], C::kTileBytes);
-          mbar_arrive_expect_tx(&v_full[st], C::kTileBytes);
         }
         __syncwarp();
-        if (loads) {
-          tma_load_3d(sK + st * C::kTileBytes + box_off, &p.mk, &k_full[st], 64 * sub, y, z);
-          tma_load_3d(sV + st * C::kTileBytes + box_off, &p.mv, &v_full[st], 64 * sub, y, z);
+        if (loads) tma_load_3d(sK + kv % NB * C::kTileBytes + box_off, &p.mk, &k_full[st], 64 * sub, y, z);
+        if (ONE && from >= 0) {
+          ok = mbar_wait_bounded(&kv_empty[fs], (from / kStages) & 1, abort_v, kWaitLimitNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
+        if (lane == 0) mbar_arrive_expect_tx(&v_full[st], C::kTileBytes);
+        __syncwarp();
+        if (loads) tma_load_3d(sV + kv % NB * C::kTileBytes + box_off, &p.mv, &v_full[st], 64 * sub, y, z);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kMma) {
     // ------------------------------------------------------------ MMAs
     // The whole warp walks the steps and one thread issues, see elect_one.
-    setmaxnreg_dec<kRegsControl>();
+    setmaxnreg_dec<kDec>();
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, 128, false);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, true);
     const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16);
@@ -485,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
       const int st = g % kStages;
       if (!wait(&k_full[st], (g / kStages) & 1)) return false;
       tc_fence_after();
-      const uint32_t qd = q_lo + x * (C::kTileBytes >> 4), kd = k_lo + st * (C::kTileBytes >> 4);
+      const uint32_t qd = q_lo + x * (C::kTileBytes >> 4), kd = k_lo + g % NB * (C::kTileBytes >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -493,41 +521,45 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           umma_ss_lo(tm + C::s_col(x), qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[x]);
+        if (ONE) umma_commit(&k_empty[st]);
         if (last) umma_commit(&q_empty[x]);
       }
       __syncwarp();
       return true;
     };
     while (ok && walk.next(p, pc)) {
-      int a[2], e[2];
+      int a[2] = {0, 0}, e[2] = {0, 0};
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < NX; ++x) {
         const Half h = half_of(p, pc, x);
         a[x] = uniform(h.a);
         e[x] = uniform(h.e);
       }
       const int j0 = uniform(pc.j0), j1 = uniform(pc.j1);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < NX; ++x) {
         if (!ok || e[x] <= a[x]) continue;
         ok = wait(&q_full[x], qwaits[x]++ & 1);
       }
       for (int j = j0; ok && j < j1; ++j, ++kv) {
         const int st = kv % kStages;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < NX; ++x)
           if (ok && j == a[x] && a[x] < e[x]) ok = issue_qk(x, kv, j == e[x] - 1);
         if (!ok) break;
         if (!wait(&v_ready[st], (kv / kStages) & 1)) { ok = false; break; }
         const bool any = (j >= a[0] && j < e[0]) || (j >= a[1] && j < e[1]);
         if (!any) {                        // nobody reads the tile; its K must have landed too
           ok = wait(&k_full[st], (kv / kStages) & 1);
-          if (lane == 0) mbar_arrive(&kv_empty[st]);
+          if (lane == 0) {
+            mbar_arrive(&kv_empty[st]);
+            if (ONE) mbar_arrive(&k_empty[st]);
+          }
           continue;
         }
-        const uint32_t vd = v_lo + st * (C::kTileBytes >> 4);
+        const uint32_t vd = v_lo + kv % NB * (C::kTileBytes >> 4);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < NX; ++x) {
           if (!ok || j < a[x] || j >= e[x]) continue;
           const uint32_t add = j > a[x] ? 1u : 0u;
           if (!wait(&p_half[x], pwaits[x] & 1)) { ok = false; break; }
@@ -546,17 +578,18 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
             for (int kk = kTile / 32; kk < kTile / 16; ++kk)
               umma_ts_lo(tm + C::o_col(x), tm + C::s_col(x) + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv, 1u);
             if (j == e[x] - 1) umma_commit(&o_full[x]);
+            if (ONE) umma_commit(&kv_empty[st]);
           }
           __syncwarp();
           if (j < e[x] - 1) ok = issue_qk(x, kv + 1, j + 1 == e[x] - 1);
         }
-        if (elect_one()) umma_commit(&kv_empty[st]);
+        if (!ONE && elect_one()) umma_commit(&kv_empty[st]);
         __syncwarp();
       }
     }
-  } else if (warp == 10) {
+  } else if (warp == kClear) {
     // ------------------------------------------------------------ values outside the unit's keys
-    setmaxnreg_dec<kRegsControl>();
+    setmaxnreg_dec<kDec>();
     int kv = 0;
     bool ok = true;
     Walk walk(p, own);
@@ -574,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
           for (int i = lane; i < kTile * (D / 8); i += 32) {
             const int row = i / (D / 8), c = i % (D / 8);
             if (key0 + row < lo || key0 + row >= hi)       // a whole row: its swizzle does not matter
-              *reinterpret_cast<uint4*>(sV + st * C::kTileBytes + (c / 8) * kSub + row * 128 + (c % 8) * 16) =
+              *reinterpret_cast<uint4*>(sV + kv % NB * C::kTileBytes + (c / 8) * kSub + row * 128 + (c % 8) * 16) =
                   make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -583,11 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&v_ready[st]);
       }
     }
-  } else if (warp == 11) {
-    setmaxnreg_dec<kRegsControl>();
+  } else if (warp > kClear) {
+    setmaxnreg_dec<kDec>();
   } else {
     // ------------------------------------------------------------ softmax
-    setmaxnreg_inc<kRegsSoftmax>();
+    setmaxnreg_inc<kInc>();
     const int x = warp >> 2;
     const int row = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -624,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
         if (!mbar_wait_bounded(&s_full[x], it & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
         // the phase that published `missing` is over: this orders the read below after it
         if (!mbar_wait_bounded(&k_full[g % kStages], (g / kStages) & 1, abort_v, kWaitLimitNs)) { ok = false; break; }
-        const uint32_t miss = missing[g % kStages];
+        const uint32_t miss = shared.missing[g % kStages];
         tc_fence_after();
         uint32_t xr[kTile];
 #pragma unroll
@@ -795,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
 
   tc_fence_before();
   __syncthreads();
-  if (abort_flag) {
+  if (shared.abort_flag) {
     // A bounded wait expired: report it, then give copies and MMAs still in flight time to
     // land before TMEM and shared memory are released.
     if (tid == 0) {
@@ -806,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const __grid_c
     }
     __syncthreads();
   }
-  if (warp == 9) {
+  if (warp == kMma) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
@@ -880,8 +913,17 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
 
 size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
+template <int D, bool CAP, bool ONE>
+cudaError_t launch_units(const ChunkParams& p, cudaLaunchConfig_t cfg) {
+  const cudaError_t e = allow_smem<&cache_chunk_kernel<D, CAP, ONE>>((int)ChunkCfg<D, ONE>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cfg.blockDim = dim3(ONE ? kOneThreads : kThreads);
+  cfg.dynamicSmemBytes = ChunkCfg<D, ONE>::kSmemBytes;
+  return cudaLaunchKernelEx(&cfg, cache_chunk_kernel<D, CAP, ONE>, p);
+}
+
 template <int D>
-cudaError_t launch_chunk(const ChunkParams& p, bool split, cudaStream_t s) {
+cudaError_t launch_chunk(const ChunkParams& p, const ChunkSplit& t, cudaStream_t s) {
   cudaError_t e;
   if (!p.direct) {
     chunk_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
@@ -889,22 +931,17 @@ cudaError_t launch_chunk(const ChunkParams& p, bool split, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const bool cap = p.a.softcap > 0.f;
-  e = cap ? allow_smem<&cache_chunk_kernel<D, true>>((int)ChunkCfg<D>::kSmemBytes)
-          : allow_smem<&cache_chunk_kernel<D, false>>((int)ChunkCfg<D>::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  auto kern = cap ? cache_chunk_kernel<D, true> : cache_chunk_kernel<D, false>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.num_runs);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = ChunkCfg<D>::kSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = p.direct ? 0 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess || !split || p.num_runs < 2) return e;
+  e = t.one ? (cap ? launch_units<D, true, true>(p, cfg) : launch_units<D, false, true>(p, cfg))
+            : (cap ? launch_units<D, true, false>(p, cfg) : launch_units<D, false, false>(p, cfg));
+  if (e != cudaSuccess || !t.split || p.num_runs < 2) return e;
   cfg.gridDim = dim3(p.num_runs - 1, kUnitRows / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
@@ -913,7 +950,8 @@ cudaError_t launch_chunk(const ChunkParams& p, bool split, cudaStream_t s) {
 
 }  // namespace
 
-ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int max_len, int window) {
+ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int max_tokens, int max_len,
+                       int window) {
   ChunkSplit t = {};
   t.tile_tokens = kTile / G;
   t.box = 16;
@@ -924,19 +962,26 @@ ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int m
   // Where the units leave half the GPU idle, the long ones among them are cut after all: 256
   // tokens over 1900 keys (8/8 heads) 43 -> 27 us, 16 over 2000 (32/8) 39 -> 23, while 900
   // over 950 (4/1, 8 tiles a unit) take 23 a block each and 29 cut.
+  // Sequences of one query tile each (small) have units of one, two blocks an SM, where these are
+  // enough for all blocks uncut or leave each a long run: 34 x 76 tokens over 3713 keys, 12
+  // heads, D = 64, 174 -> 118 us, 8 x 16 over 8192 (32/8) 76 -> 70; 16 x 64 over 2000 (8 heads) 39,
+  // with the cuts that two blocks an SM would need 49.
+  const bool small = max_tokens <= t.tile_tokens;
   for (int tiles_per_unit = 1; tiles_per_unit <= 2; ++tiles_per_unit) {
     t.unit_tokens = tiles_per_unit * t.tile_tokens;
-    t.max_entries = (int)(T / t.unit_tokens + std::min<long long>(B, T));
+    t.max_entries = small ? std::min(B, T) : (int)(T / t.unit_tokens + std::min<long long>(B, T));
     // key tiles of a unit at most
     const long long reach = window < 0 ? max_len : std::min<long long>(max_len, (long long)window + t.unit_tokens);
     const long long tiles = (reach + t.box + kTile - 1) / kTile + 1;
     const long long units = (long long)t.max_entries * Hkv;
+    t.one = small && tiles_per_unit == 2 && (units >= 296 || units * tiles >= 12 * 296);
+    if (t.one) t.unit_tokens = t.tile_tokens;
     const bool few = units <= 74;
     t.short_unit = few ? kShortIfFew : kShortUnit;
     t.direct = units <= 148 && B <= 1024 && tiles <= (few ? kDirectIfFew : kShortUnit);
     t.split = !t.direct && tiles > t.short_unit;
     // two key tiles a run at least
-    t.runs = (int)std::min<long long>(148, t.direct ? units : std::max<long long>(1, units * tiles / 2));
+    t.runs = (int)std::min<long long>(t.one ? 296 : 148, t.direct ? units : std::max<long long>(1, units * tiles / 2));
     if (t.direct) break;
   }
   if (t.direct) return t;
@@ -977,7 +1022,7 @@ cudaError_t launch_cache_chunk(const CacheAttendParams& a, const ChunkSplit& t, 
   p.box = t.box;
   p.max_entries = t.max_entries;
   p.scale_log2 = a.scale * kLog2e;
-  return a.D == 64 ? launch_chunk<64>(p, t.split, s) : launch_chunk<128>(p, t.split, s);
+  return a.D == 64 ? launch_chunk<64>(p, t, s) : launch_chunk<128>(p, t, s);
 }
 
 }  // namespace swa

@@ -71,12 +71,13 @@ struct ChunkSplit {
   int unit_tokens;                  // tokens of a unit: one query tile's or two's
   int short_unit;                   // units of up to so many key tiles are not cut
   bool direct;                      // a block a unit, no list of work
+  bool one;                         // units of one query tile, two blocks an SM
   int box;                          // keys of one load: they lie in one page
   int max_entries;                  // units of all sequences, for one KV head
   bool split;                       // units long enough to be parted between blocks
   size_t bytes;                     // workspace
 };
-ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int max_len, int window);
+ChunkSplit chunk_split(int B, int T, int Hkv, int G, int D, int page_size, int max_tokens, int max_len, int window);
 cudaError_t launch_cache_chunk(const CacheAttendParams& p, const ChunkSplit& t, void* workspace, cudaStream_t s);
 
 }  // namespace swa

@@ -316,6 +316,10 @@ ATTENDS = [
     ("chunk_long", BF16, 4, 1, 128, 128, None, 0.0, [260], [3001]),
     ("chunk_few", BF16, 8, 2, 64, 32, None, 20.0, [70, 33], [1900, 1500]),
     ("chunk_many_parts", BF16, 8, 1, 128, 64, None, 0.0, [9], [9001]),
+    ("one_tile", BF16, 32, 8, 128, 16, None, 0.0, [1 + 7 * i % 32 for i in range(40)], [33 + 29 * i % 300 for i in range(40)]),
+    ("one_tile_window", BF16, 15, 5, 64, 48, 70, 20.0, [11 + i % 31 for i in range(60)], [41 + 17 * i % 400 for i in range(60)]),
+    ("one_tile_long", BF16, 36, 12, 64, 64, None, 0.0, [12, 1, 42, 0, 5, 12, 12, 30], [4800, 300, 42, 0, 5, 999, 2000, 31]),
+    ("one_tile_long_cap", BF16, 24, 8, 128, 32, 5000, 9.0, [20, 40] + [3] * 9, [6000, 700] + [40] * 9),
     ("sequences_600", BF16, 2, 1, 64, 16, None, 0.0, [1] * 600, [1 + 7 * i % 41 for i in range(600)]),
     ("sequences_600_rows_40", BF16, 8, 1, 64, 16, 20, 0.0, [5] * 599 + [6], [6 + 7 * i % 41 for i in range(600)]),
     ("heads_128", BF16, 128, 1, 64, 32, None, 0.0, [3], [77]),

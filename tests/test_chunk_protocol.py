@@ -18,7 +18,7 @@ NS = 2                                     # ring slots
 THREADS = 3                                # softmax threads of a group (128 on the GPU)
 
 
-def random_pieces(rng, n):
+def random_pieces(rng, n, one=False):
     """(j0, j1, [(a, e), (a, e)]): a piece's steps and what each query tile uses of them."""
     out = []
     for _ in range(n):
@@ -26,7 +26,7 @@ def random_pieces(rng, n):
         j1 = j0 + rng.randrange(1, 7)
         tiles = []
         for x in range(2):
-            if rng.random() < (0.05 if x == 0 else 0.25):
+            if (one and x == 1) or rng.random() < (0.05 if x == 0 else 0.25):
                 tiles.append((j0, j0))     # a tile without a step in the piece
             else:
                 a = rng.randrange(j0, j1)
@@ -35,8 +35,9 @@ def random_pieces(rng, n):
     return out
 
 
-def simulate(pieces, rng, mistake=None):
-    bars = {}
+def simulate(pieces, rng, mistake=None, one=False):
+    """``one``: units of one query tile, one buffer of K and one of V that are freed apart."""
+    bars, NB = {}, 1 if one else NS
 
     def bar(name, count=1):
         return bars.setdefault(name, Barrier(name, count))
@@ -47,10 +48,10 @@ def simulate(pieces, rng, mistake=None):
         for name in ("p_half", "p_full"):
             bar((name, x), THREADS)
     for s in range(NS):
-        for name in ("k_full", "v_full", "v_ready", "kv_empty"):
+        for name in ("k_full", "v_full", "v_ready", "kv_empty", "k_empty"):
             bar((name, s))
     loads, products, commits = [], [], []  # in flight
-    q, k, v = [None, None], [None] * NS, [None] * NS      # what lies in shared memory
+    q, k, v = [None, None], [None] * NB, [None] * NB      # what lies in shared memory
     S, P, O = [None, None], [None, None], [[], []]        # and in TMEM
     read = [0, 0]                          # threads that have read the S of the step
     results = []
@@ -72,10 +73,13 @@ def simulate(pieces, rng, mistake=None):
                     land(q, x, i, bar(("q_full", x)))
             for j in range(j0, j1):
                 st = kv % NS
-                if kv >= NS:
-                    yield from wait(bar(("kv_empty", st)), kv // NS - 1)
-                land(k, st, (i, j), bar(("k_full", st)))
-                land(v, st, (i, j, "raw"), bar(("v_full", st)))
+                was = kv - NB              # the step whose buffers these are
+                if was >= 0:
+                    yield from wait(bar(("k_empty" if one else "kv_empty", was % NS)), was // NS)
+                land(k, kv % NB, (i, j), bar(("k_full", st)))
+                if one and was >= 0 and mistake != "early V":
+                    yield from wait(bar(("kv_empty", was % NS)), was // NS)
+                land(v, kv % NB, (i, j, "raw"), bar(("v_full", st)))
                 kv += 1
                 yield
 
@@ -85,8 +89,8 @@ def simulate(pieces, rng, mistake=None):
             for j in range(j0, j1):
                 st = kv % NS
                 yield from wait(bar(("v_full", st)), kv // NS)
-                assert v[st] == (i, j, "raw")
-                v[st] = (i, j, "clean")
+                assert v[kv % NB] == (i, j, "raw")
+                v[kv % NB] = (i, j, "clean")
                 bar(("v_ready", st)).arrive()
                 kv += 1
                 yield
@@ -102,8 +106,8 @@ def simulate(pieces, rng, mistake=None):
             yield from wait(bar(("k_full", st)), g // NS)
 
             def run():
-                if k[st] != (i, j) or q[x] != i:
-                    raise ProtocolError(f"S of {(i, j)} from K {k[st]} and Q {q[x]}")
+                if k[g % NB] != (i, j) or q[x] != i:
+                    raise ProtocolError(f"S of {(i, j)} from K {k[g % NB]} and Q {q[x]}")
                 if S[x] is not None and read[x] < THREADS:
                     raise ProtocolError("S overwritten before every thread has read it")
                 if P[x] is not None:
@@ -111,15 +115,17 @@ def simulate(pieces, rng, mistake=None):
                 S[x], read[x] = (i, j), 0
             products.append(("mma", run))
             commit(("s_full", x))
+            if one:
+                commit(("k_empty", st))
             if last:
                 commit(("q_empty", x))
 
-        def pv(x, i, j, st, first):
+        def pv(x, i, j, buffer, first):
             def run():
                 if P[x] != (i, j):
                     raise ProtocolError(f"P {P[x]} for {(i, j)}")
-                if v[st] != (i, j, "clean"):
-                    raise ProtocolError(f"V {v[st]} for {(i, j)}")
+                if v[buffer] != (i, j, "clean"):
+                    raise ProtocolError(f"V {v[buffer]} for {(i, j)}")
                 O[x] = [(i, j)] if first else O[x] + [(i, j)]
                 P[x] = S[x] = None
             return run
@@ -140,6 +146,8 @@ def simulate(pieces, rng, mistake=None):
                     if mistake != "unused K":
                         yield from wait(bar(("k_full", st)), kv // NS)
                     bar(("kv_empty", st)).arrive()
+                    if one:
+                        bar(("k_empty", st)).arrive()
                     kv += 1
                     continue
                 for x in range(2):
@@ -151,14 +159,19 @@ def simulate(pieces, rng, mistake=None):
                         yield from wait(bar(("p_full", x)), pw[x])
                     pw[x] += 1
 
-                    products.append(("mma", pv(x, i, j, st, j == a)))
+                    products.append(("mma", pv(x, i, j, kv % NB, j == a)))
                     if j == e - 1:
                         commit(("o_full", x))
+                    if one:
+                        commit(("kv_empty", st))
+                    if j == e - 1:
+                        pass
                     elif mistake == "no QK":
                         pass
                     else:
                         yield from qk(x, i, kv + 1, j + 1, j + 1 == e - 1)
-                products.append(("commit", bar(("kv_empty", st))))
+                if not one:
+                    commit(("kv_empty", st))
                 kv += 1
                 yield
 
@@ -213,20 +226,22 @@ def simulate(pieces, rng, mistake=None):
     assert sorted(results) == sorted((x, i) for i, p in enumerate(pieces) for x in range(2) if p[2][x][0] < p[2][x][1])
 
 
+@pytest.mark.parametrize("one", [False, True])
 @pytest.mark.parametrize("seed", range(60))
-def test_protocol(seed):
+def test_protocol(seed, one):
     rng = random.Random(seed)
-    simulate(random_pieces(rng, rng.randrange(1, 9)), rng)
+    simulate(random_pieces(rng, rng.randrange(1, 9), one), rng, one=one)
 
 
-@pytest.mark.parametrize("mistake", ["early PV", "no QK", "unused K"])
-def test_planted_mistakes_are_found(mistake):
+@pytest.mark.parametrize("mistake,one", [("early PV", False), ("no QK", False), ("unused K", False), ("early V", True),
+                                         ("early PV", True), ("no QK", True)])
+def test_planted_mistakes_are_found(mistake, one):
     found = 0
     for seed in range(60):
         rng = random.Random(1000 + seed)
-        pieces = random_pieces(rng, 8)
+        pieces = random_pieces(rng, 8, one)
         try:
-            simulate(pieces, rng, mistake)
+            simulate(pieces, rng, mistake, one)
         except AssertionError:
             found += 1
     assert found > 0
