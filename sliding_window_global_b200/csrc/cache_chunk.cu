@@ -23,9 +23,8 @@
 // the measured burst rate); six ragged chunks of up to 2048 tokens in a 512-key window 105 us.
 //
 // A capped score is cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), so three of its
-// operations want the MUFU instead of one: a quarter of the exponentials go to the FMA pipe there (a
-// 4096-token chunk over 16384 keys 1546 us; 1566 with half of them). Registers are split so that this
-// form spills none either (200 a softmax thread: 1622 us).
+// operations want the MUFU instead of one. Exponentials by a polynomial on the FMA pipe (1e-4 off)
+// would gain a few per cent and show in the lse: they stay on the MUFU.
 //
 // Warp roles (ONE has no tile B: 4 loads and so on): 0-3 softmax of tile A, 4-7 of tile B, 8 loads, 9 MMAs, 10 zeroes the values at
 // positions outside the unit's keys (P is 0 there, but 0 times a NaN would not be).
@@ -55,7 +54,6 @@ constexpr int kShortUnit = 16;                            // units of up to so m
 constexpr int kShortIfFew = 6, kDirectIfFew = 12;         // where they fill half the GPU at most: see chunk_split
 constexpr int kMinPiece = 4;                              // nor is a unit cut this close to its ends
 constexpr int kUnitRows = 2 * kTile;
-constexpr int kCapPoly = 8;                            // exponentials of 32 on the FMA pipe where scores are capped
 
 // The tokens of a unit: a pair of query tiles of a sequence, or one (unit_tokens).
 struct ChunkEntry {
@@ -341,19 +339,16 @@ static_assert(ChunkCfg<128, false>::kSmemBytes <= 227 * 1024 && 2 * (ChunkCfg<12
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// The largest score of a row; with KEEP a NaN where there is one.
-template <bool KEEP>
 __device__ __forceinline__ float row_max(const float (&x)[kTile]) {
-  const auto max3 = [](float a, float b, float c) { return KEEP ? fmax3_nan(a, b, c) : fmax3(a, b, c); };
   float m[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m[i] = max3(x[i], x[i], x[8 + i]);
+  for (int i = 0; i < 8; ++i) m[i] = fmaxf(x[i], x[8 + i]);
 #pragma unroll
   for (int e = 16; e < kTile; e += 16) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = max3(m[i], x[e + i], x[e + 8 + i]);
+    for (int i = 0; i < 8; ++i) m[i] = fmax3(m[i], x[e + i], x[e + 8 + i]);
   }
-  return max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), max3(m[6], m[7], m[7]));
+  return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
 template <int D, bool CAP, bool ONE>
@@ -694,9 +689,7 @@ cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
           }
         }
         const float mul = CAP ? 1.f : sl2;
-        const float most = row_max<CAP>(s);
-        const bool nan = CAP && most != most;      // which the polynomial would lose
-        const float m_new = fmaxf(m, nan ? 0.f : most * mul);
+        const float m_new = fmaxf(m, row_max(s) * mul);
         const bool need = (m == -INFINITY) ? (m_new > -INFINITY) : (m_new > m + kRescaleThreshold);
         const bool rescale = __any_sync(0xffffffffu, need);
         float alpha = 1.f;
@@ -732,15 +725,10 @@ cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
               float a0, a1, a2, a3;
               ffma2(a0, a1, s[e], s[e + 1], mul, mul, neg_m, neg_m);
               ffma2(a2, a3, s[e + 2], s[e + 3], mul, mul, neg_m, neg_m);
-              if (CAP && q < kCapPoly) {
-                exp2_poly2(a0, a1, a0, a1);
-                exp2_poly2(a2, a3, a2, a3);
-              } else {
-                a0 = ex2_approx(a0);
-                a1 = ex2_approx(a1);
-                a2 = ex2_approx(a2);
-                a3 = ex2_approx(a3);
-              }
+              a0 = ex2_approx(a0);
+              a1 = ex2_approx(a1);
+              a2 = ex2_approx(a2);
+              a3 = ex2_approx(a3);
               fadd2(acc0, acc1, acc0, acc1, a0, a1);
               fadd2(acc2, acc3, acc2, acc3, a2, a3);
               // P in bf16, the type of the product that follows; the sum keeps 32 bits
@@ -756,7 +744,6 @@ cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
           }
         }
         l += (acc0 + acc1) + (acc2 + acc3);
-        if (nan) l = most;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[x]);

@@ -35,12 +35,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {   // NaN if one is
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 // 2^a for a pair of arguments <= 2^7 on the FMA pipe: round to the nearest
 // integer i (adding 1.5*2^23 leaves i in the low mantissa bits), f = a - i in
 // [-1/2, 1/2], 2^f by a degree-3 polynomial (coefficients fitted for this
