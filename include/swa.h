@@ -522,6 +522,14 @@ swa_status swa_cache_attend(const swa_cache* cache, const swa_cache_batch* batch
 size_t swa_cache_attend_workspace_bytes(const swa_cache* cache, const swa_cache_batch* batch,
                                         const swa_cache_attend_args* args);
 
+/* Self-test of the look-ups of the kernel that serves calls of few new tokens in bf16 (an
+ * addition of this library: the pages describe nothing like it), on the host and with the
+ * kernel's own functions: columns[2b] and columns[2b + 1] (HOST [B, 2]) receive the first
+ * and the last block_table column that it reads for sequence b, -1 and -1 where it reads
+ * none.  seq_lens and cu_tokens are HOST arrays here; no other pointer is followed. */
+swa_status swa_selftest_token_columns(const swa_cache* cache, const swa_cache_batch* batch,
+                                      const swa_cache_attend_args* args, int32_t* columns);
+
 /* Synchronise `stream`, read the cache's error word and clear it: SWA_OK,
  * SWA_ERR_DEVICE_CHECK, SWA_ERR_TIMEOUT or SWA_ERR_CUDA. */
 swa_status swa_cache_check(const swa_cache* cache, void* stream);

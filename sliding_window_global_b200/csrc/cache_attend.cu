@@ -665,6 +665,33 @@ swa_status attend_bounds(const swa_cache& c, const swa_cache_batch& b, const swa
   return SWA_OK;
 }
 
+// The parameter block of a checked call but for the bounds and the workspace.
+void fill_params(const swa_cache& c, const swa_cache_batch& b, const swa_cache_attend_args& a, CacheAttendParams* p) {
+  p->k_pages = c.k_pages;
+  p->v_pages = c.v_pages;
+  p->q = a.q;
+  p->out = a.out;
+  p->lse = a.lse;
+  p->block_table = b.block_table;
+  p->seq_lens = b.seq_lens;
+  p->cu_tokens = b.cu_tokens;
+  p->err = c.error_word;
+  p->q_token = a.q_stride[0];
+  p->q_head = a.q_stride[1];
+  p->B = b.batch;
+  p->T = b.num_tokens;
+  p->Hq = a.num_q_heads;
+  p->Hkv = c.num_kv_heads;
+  p->G = p->Hq / p->Hkv;
+  p->D = c.head_dim;
+  p->num_pages = c.num_pages;
+  p->page_size = c.page_size;
+  p->max_pages = b.max_pages;
+  p->window = a.window;
+  p->scale = a.scale == 0.f ? 1.f / sqrtf((float)p->D) : a.scale;
+  p->softcap = a.softcap;
+}
+
 }  // namespace
 
 swa_status check_cache(const swa_cache& c) {
@@ -712,30 +739,8 @@ swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const 
       (a->num_q_heads > 1 && (a->q_stride[1] <= 0 || a->q_stride[1] % unit)))
     return SWA_ERR_INVALID_ARG;
   const swa::AttendSplit sp = swa::attend_split(*c, *b, *a, p.max_tokens, p.max_len);
-  p.k_pages = c->k_pages;
-  p.v_pages = c->v_pages;
-  p.q = a->q;
-  p.out = a->out;
-  p.lse = a->lse;
-  p.block_table = b->block_table;
-  p.seq_lens = b->seq_lens;
-  p.cu_tokens = b->cu_tokens;
-  p.err = c->error_word;
-  p.q_token = a->q_stride[0];
-  p.q_head = a->q_stride[1];
-  p.B = b->batch;
-  p.T = b->num_tokens;
-  p.Hq = a->num_q_heads;
-  p.Hkv = c->num_kv_heads;
-  p.G = p.Hq / p.Hkv;
-  p.D = c->head_dim;
-  p.num_pages = c->num_pages;
-  p.page_size = c->page_size;
-  p.max_pages = b->max_pages;
-  p.window = a->window;
+  swa::fill_params(*c, *b, *a, &p);
   p.nsplit = sp.nsplit;
-  p.scale = a->scale == 0.f ? 1.f / sqrtf((float)p.D) : a->scale;
-  p.softcap = a->softcap;
   if (sp.bytes && (!a->workspace || !swa::aligned16(a->workspace) || a->workspace_bytes < sp.bytes))
     return SWA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -757,6 +762,18 @@ swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const 
                 : swa::launch_core<128>(p, sp.tile_rows, sp.row_tiles, s);
   if (e == cudaSuccess && p.nsplit > 1) e = swa::launch_merge(p, s);
   return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+swa_status swa_selftest_token_columns(const swa_cache* c, const swa_cache_batch* b, const swa_cache_attend_args* a,
+                                      int32_t* columns) {
+  swa::CacheAttendParams p = {};
+  if (!c || !b || !a || !columns) return SWA_ERR_INVALID_ARG;
+  const swa_status st = swa::attend_bounds(*c, *b, *a, &p.max_tokens, &p.max_len);
+  if (st != SWA_OK) return st;
+  if (b->batch == 0 || b->num_tokens == 0) return SWA_OK;
+  swa::fill_params(*c, *b, *a, &p);
+  swa::token_columns(p, columns);
+  return SWA_OK;
 }
 
 swa_status swa_cache_check(const swa_cache* c, void* stream) {

@@ -64,6 +64,10 @@ struct TokenSplit {
 TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach);
 cudaError_t launch_cache_token(CacheAttendParams p, const TokenSplit& t, void* workspace, cudaStream_t s);
 
+// First and last block-table column that kernel looks up for each sequence (-1, -1: none),
+// computed on the host; p's index arrays are host memory.
+void token_columns(const CacheAttendParams& p, int32_t* columns);
+
 // The many-token kernel (bf16): how its work is laid out, from sizes only.
 struct ChunkSplit {
   int runs;                         // blocks, each with an equal run of key tiles

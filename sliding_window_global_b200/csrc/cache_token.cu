@@ -68,24 +68,31 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 // The steps of a sequence (the same for each of its KV heads): keys [lo, hi) of interest,
 // steps from the step-aligned start on.  A sequence with new tokens has one at least, so
-// that rows without a key are written too.
+// that rows without a key are written too; without any key at all (a length beyond the
+// call's bounds can put the windows there) nothing is looked up for it.
 struct TokenUnit {
   CacheSeq s;
   int lo, hi, base, steps;
 };
 
 template <int D>
-__device__ __forceinline__ TokenUnit token_unit(const CacheAttendParams& p, int b) {
+__host__ __device__ __forceinline__ TokenUnit token_unit(const CacheAttendParams& p, int b) {
   TokenUnit u;
   u.s = cache_seq(p, b);
   u.lo = u.hi = u.base = u.steps = 0;
   if (u.s.count > 0) {
     u.lo = key_begin(p, u.s, 0);
-    u.hi = max(u.lo, key_end(u.s, u.s.count - 1));
+    u.hi = key_end(u.s, u.s.count - 1);
+    if (u.hi <= u.lo) u.lo = u.hi = 0;
     u.base = u.lo / Step<D>::kKeys * Step<D>::kKeys;
     u.steps = max(1, (u.hi - u.base + Step<D>::kKeys - 1) / Step<D>::kKeys);
   }
   return u;
+}
+
+// The block-table column of the 16-key group that begins at `key`, < 0: nothing to look up.
+__host__ __device__ __forceinline__ int group_column(const CacheAttendParams& p, const TokenUnit& u, int key) {
+  return key < u.hi ? key / p.page_size : -1;
 }
 
 // Sum of the steps of all units, by one warp (below 2^31, checked on the host); each lane
@@ -311,8 +318,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
   auto look_up = [&]() {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const int key = fu.base + fj * S::kKeys + 16 * g;
-      fpage[g] = key < fu.hi ? __ldg(p.block_table + (long long)fb * p.max_pages + key / p.page_size) : 0;
+      const int col = group_column(p, fu, fu.base + fj * S::kKeys + 16 * g);
+      fpage[g] = col < 0 ? 0 : load_index(p.block_table + (long long)fb * p.max_pages + col);
     }
   };
   if (total > 0) look_up();
@@ -702,6 +709,23 @@ TokenSplit token_split(int B, int Hkv, int D, int rows, long long reach) {
   t.blocks = (int)((want + t.warps - 1) / t.warps);
   t.bytes = (((size_t)B + 1) * 4 + 15) / 16 * 16 + (size_t)2 * t.blocks * t.warps * t.row_pad * (D + 1) * 4;
   return t;
+}
+
+template <int D>
+static void unit_columns(const CacheAttendParams& p, int b, int32_t* first_last) {
+  const TokenUnit u = token_unit<D>(p, b);
+  first_last[0] = first_last[1] = -1;
+  for (int j = 0; j < u.steps; ++j)
+    for (int g = 0; g < Step<D>::kGroups; ++g) {
+      const int col = group_column(p, u, u.base + j * Step<D>::kKeys + 16 * g);
+      if (col < 0) continue;
+      if (first_last[0] < 0) first_last[0] = col;
+      first_last[1] = col;
+    }
+}
+
+void token_columns(const CacheAttendParams& p, int32_t* columns) {
+  for (int b = 0; b < p.B; ++b) p.D == 64 ? unit_columns<64>(p, b, columns + 2 * b) : unit_columns<128>(p, b, columns + 2 * b);
 }
 
 cudaError_t launch_cache_token(CacheAttendParams p, const TokenSplit& t, void* workspace, cudaStream_t s) {

@@ -33,6 +33,7 @@ EXPORTS = (
     "swa_forward_ex", "swa_bucket_local_bias", "swa_backward", "swa_selftest_wait_timeout",
     "swa_selftest_exp2_poly", "swa_rotary_forward", "swa_rotary_backward", "swa_rotary_workspace_bytes",
     "swa_cache_append", "swa_cache_attend", "swa_cache_attend_workspace_bytes", "swa_cache_check",
+    "swa_selftest_token_columns",
 )
 
 
@@ -140,6 +141,8 @@ def load_library():
         lib.swa_cache_attend.restype = I
         lib.swa_cache_attend_workspace_bytes.argtypes = [P, P, P]
         lib.swa_cache_attend_workspace_bytes.restype = U64
+        lib.swa_selftest_token_columns.argtypes = [P, P, P, P]
+        lib.swa_selftest_token_columns.restype = I
         lib.swa_cache_check.argtypes = [P, P]
         lib.swa_cache_check.restype = I
         _lib = lib

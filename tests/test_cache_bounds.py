@@ -1,0 +1,86 @@
+"""Bounds of the paged cache's calls: which block-table entries the kernels read, lengths
+and capacities at the edge of what an int32 holds."""
+import ctypes
+import random
+
+import pytest
+import torch
+
+from sliding_window_global_b200 import load_library
+from sliding_window_global_b200.cache import Cache, CacheAttendArgs, CacheBatch
+from tests.test_cache import _problem, check_attention, reference
+
+DEVICE_CHECK = 6
+BF16, FP32 = torch.bfloat16, torch.float32
+
+_BUF = ctypes.create_string_buffer(512)
+_PTR = (ctypes.addressof(_BUF) + 255) & ~255          # stands for device memory that no host call reads
+
+
+def looked_up(D, page, max_pages, lens, new, window, max_len, max_tokens):
+    """First and last block-table column that the few-token kernel reads of each sequence."""
+    B, cu = len(lens), [0]
+    for c in new:
+        cu.append(cu[-1] + c)
+    lens, cu = (ctypes.c_int32 * B)(*lens), (ctypes.c_int32 * (B + 1))(*cu)
+    c = Cache(_PTR, _PTR, 8, 1, page, D, 0, _PTR)
+    b = CacheBatch(B, cu[B], _PTR, max_pages, ctypes.addressof(lens), ctypes.addressof(cu))
+    a = CacheAttendArgs(num_q_heads=4, q=_PTR, q_stride0=256, q_stride1=64, max_tokens=max_tokens, max_len=max_len,
+                        window=window, out=_PTR)
+    columns = (ctypes.c_int32 * (2 * B))()
+    lib = load_library()
+    assert lib.swa_selftest_token_columns(ctypes.byref(c), ctypes.byref(b), ctypes.byref(a), columns) == 0
+    return [(columns[2 * i], columns[2 * i + 1]) for i in range(B)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_no_length_leads_outside_the_table(D):
+    """seq_lens is device memory that nobody has checked: whatever it holds, only columns of
+    the table are read, and none for a window that lies behind the bound on lengths."""
+    assert looked_up(D, 16, 64, [5001], [1], 511, 1024, 1) == [(-1, -1)]
+    assert looked_up(D, 16, 64, [2 ** 31 - 1], [1], 511, 0, 1) == [(-1, -1)]
+    assert looked_up(D, 16, 64, [1030], [2], 511, 0, 2)[0] == ((1028 - 511) // 16, 63)
+    rng = random.Random(D)
+    for _ in range(3000):
+        page, columns = rng.choice([16, 48, 64]), rng.randint(1, 40)
+        capacity = page * columns
+        max_len = rng.choice([0, rng.randint(1, capacity), capacity, 4 * capacity])
+        new = [rng.randint(0, 9) for _ in range(3)]
+        lens = [rng.choice([rng.randint(-20, 2 * capacity), rng.randint(0, capacity), 2 ** 31 - 1 - rng.randint(0, 40),
+                            -2 ** 31 + rng.randint(0, 40), rng.randint(-2 ** 31, 2 ** 31 - 1)]) for _ in range(3)]
+        window = rng.choice([-1, 0, rng.randint(1, 2 * capacity), 2 ** 31 - 1])
+        for first, last in looked_up(D, page, columns, lens, new, window, max_len, rng.randint(1, 9)):
+            assert -1 <= first <= last < columns and (first >= 0) == (last >= 0)
+
+
+# kernels: few tokens (clusters, runs), many tokens (with a list of units, without), fp32 few and many
+KERNELS = [
+    ("cluster", BF16, 4, 1, 64, 16, 100, [1, 2, 1], [300, 200, 77]),
+    ("runs", BF16, 4, 1, 128, 64, 5000, [1] * 40, [1 + 977 * i % 2999 for i in range(39)] + [12000]),
+    ("chunks", BF16, 4, 2, 128, 48, 100, [200, 90, 1], [900, 500, 333]),
+    ("one_chunk", BF16, 8, 1, 64, 16, 50, [20, 30], [300, 200]),
+    ("fp32_tokens", FP32, 4, 1, 128, 16, 100, [1, 2, 1], [300, 200, 77]),
+    ("fp32_chunks", FP32, 2, 2, 64, 48, 100, [70, 3], [400, 333]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", KERNELS, ids=[c[0] for c in KERNELS])
+@pytest.mark.parametrize("beyond", [1, 4000, 2 ** 30, None])
+def test_windows_behind_the_bound_on_lengths(case, beyond):
+    """A length beyond the table, whose windows lie partly or wholly behind its last page:
+    reported; rows without a key are 0 and -inf, the other sequences as ever."""
+    name, dtype, Hq, Hkv, D, page, window, new, lens = case
+    s = _problem(dtype, Hkv, D, page, new, lens, 41)
+    q = torch.randn((s["total"], Hq, D), generator=s["g"]).to(dtype).cuda()
+    ref = reference(s, q, window, 0.0, 0.0, Hq)
+    max_len = max(lens)
+    bad = 2 ** 31 - 1 if beyond is None else max_len + window + new[0] + beyond
+    given = s["lens"].clone()
+    given[0] = bad                                        # the first of its windows begins behind max_len
+    out, lse = s["cache"].attend(q, given.cuda(), s["table"].cuda(), cu_tokens=s["cu"].cuda(), max_tokens=max(new),
+                                 max_len=max_len, window=window)
+    assert s["cache"].check() == DEVICE_CHECK and s["cache"].check() == 0
+    c = new[0]
+    assert not out[:c].any() and bool(torch.isneginf(lse[:c]).all())
+    check_attention(out[c:], lse[c:], [x[c:] for x in ref], dtype)
