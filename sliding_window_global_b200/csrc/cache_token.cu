@@ -90,9 +90,11 @@ __host__ __device__ __forceinline__ TokenUnit token_unit(const CacheAttendParams
   return u;
 }
 
-// The block-table column of the 16-key group that begins at `key`, < 0: nothing to look up.
+// The block-table column of the 16-key group that begins at `key`, < 0: nothing to look up,
+// since none of its keys is in reach. A step's first group may lie wholly before a window, in
+// a page of its own whose entry means nothing any more.
 __host__ __device__ __forceinline__ int group_column(const CacheAttendParams& p, const TokenUnit& u, int key) {
-  return key < u.hi ? key / p.page_size : -1;
+  return key < u.hi && key + 16 > u.lo ? key / p.page_size : -1;
 }
 
 // Sum of the steps of all units, by one warp (below 2^31, checked on the host); each lane

@@ -53,6 +53,19 @@ def test_no_length_leads_outside_the_table(D):
             assert -1 <= first <= last < columns and (first >= 0) == (last >= 0)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_only_pages_in_reach_are_looked_up(D):
+    """Entries of pages that no key of the call lies in may hold anything: a window that
+    begins in the second half of a step of 32 keys, in another page than its first half."""
+    assert looked_up(D, 16, 64, [1011], [1], 130, 0, 1) == [(55, 63)]
+    rng = random.Random(D + 1)
+    for _ in range(3000):
+        page, c, window = rng.choice([16, 32, 48, 80, 128]), rng.randint(1, 8), rng.randint(0, 400)
+        length = rng.randint(c, 2000)
+        keys = range(max(0, length - c - window), length)
+        assert looked_up(D, page, 2000 // page + 1, [length], [c], window, 0, c) == [(keys[0] // page, keys[-1] // page)]
+
+
 # kernels: few tokens (clusters, runs), many tokens (with a list of units, without), fp32 few and many
 KERNELS = [
     ("cluster", BF16, 4, 1, 64, 16, 100, [1, 2, 1], [300, 200, 77]),
@@ -84,3 +97,27 @@ def test_windows_behind_the_bound_on_lengths(case, beyond):
     c = new[0]
     assert not out[:c].any() and bool(torch.isneginf(lse[:c]).all())
     check_attention(out[c:], lse[c:], [x[c:] for x in ref], dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 48])
+@pytest.mark.parametrize("dtype,G,new", [(BF16, 4, [1] * 40), (BF16, 4, [1, 3, 2]), (BF16, 8, [20, 33]),
+                                         (BF16, 2, [150, 1, 70]), (FP32, 2, [1, 1, 2]), (FP32, 2, [40, 3])])
+@pytest.mark.parametrize("D", [64, 128])
+def test_entries_before_the_windows_may_hold_anything(D, dtype, G, new, page):
+    """Pages behind a sliding window given back, their entries -1 or another sequence's."""
+    B, window = len(new), 130
+    lens = [400 + 83 * i % 1201 + new[i] for i in range(B)]
+    lens[0] = 1010 + new[0]
+    s = _problem(dtype, 2, D, page, new, lens, 43)
+    q = torch.randn((s["total"], 2 * G, D), generator=s["g"]).to(dtype).cuda()
+    ref = reference(s, q, window, 0.0, 0.0, 2 * G)
+    for b in range(B):
+        gone = (lens[b] - new[b] - window) // page         # whole pages before the first window
+        s["table"][b, :gone] = -1
+        s["table"][b, :gone:3] = 2 ** 31 - 1
+    for bounds in (dict(max_tokens=max(new), max_len=max(lens)), {}):
+        out, lse = s["cache"].attend(q, s["lens"].cuda(), s["table"].cuda(), cu_tokens=s["cu"].cuda(), window=window,
+                                     **bounds)
+        assert s["cache"].check() == 0
+        check_attention(out, lse, ref, dtype)
