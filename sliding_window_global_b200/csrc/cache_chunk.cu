@@ -351,7 +351,7 @@ __device__ __forceinline__ float row_max(const float (&x)[kTile]) {
   return fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
 
-template <int D, bool CAP, bool ONE>
+template <int D, int CAP, bool ONE>
 __global__ void __launch_bounds__(ONE ? kOneThreads : kThreads, ONE ? 2 : 1)
 cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
   using C = ChunkCfg<D, ONE>;
@@ -622,8 +622,7 @@ cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
     const uint32_t s_addr = lane_base + C::s_col(x), o_addr = lane_base + C::o_col(x);
     const int tok = row / p.a.G, head = row % p.a.G;
     const float sl2 = p.scale_log2;
-    const float cap_l2 = p.a.softcap * kLog2e;
-    const float cap_in = CAP ? 2.f * sl2 / p.a.softcap : 0.f;
+    const ScoreCap<CAP> score_cap(sl2, p.a.softcap);
     int it = 0, oc = 0, kv = 0;
     bool ok = true;
     Walk walk(p, own);
@@ -664,12 +663,7 @@ cache_chunk_kernel(const __grid_constant__ ChunkParams p) {
         for (int e = 0; e < kTile; e += 2) {
           s[e] = __uint_as_float(xr[e]);
           s[e + 1] = __uint_as_float(xr[e + 1]);
-          if (CAP) {
-            float u0, u1;
-            fmul2(u0, u1, s[e], s[e + 1], cap_in, cap_in);
-            fadd2(u0, u1, ex2_approx(u0), ex2_approx(u1), 1.f, 1.f);
-            ffma2(s[e], s[e + 1], rcp_approx(u0), rcp_approx(u1), -2.f * cap_l2, -2.f * cap_l2, cap_l2, cap_l2);
-          }
+          if (CAP) score_cap.pair(s[e], s[e + 1]);
         }
         const int key0 = pc.en.base + j * kTile;
         const int lo_t = klo - key0, hi_t = khi - key0;
@@ -900,13 +894,20 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
 
 size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
-template <int D, bool CAP, bool ONE>
+template <int D, int CAP, bool ONE>
 cudaError_t launch_units(const ChunkParams& p, cudaLaunchConfig_t cfg) {
   const cudaError_t e = allow_smem<&cache_chunk_kernel<D, CAP, ONE>>((int)ChunkCfg<D, ONE>::kSmemBytes);
   if (e != cudaSuccess) return e;
   cfg.blockDim = dim3(ONE ? kOneThreads : kThreads);
   cfg.dynamicSmemBytes = ChunkCfg<D, ONE>::kSmemBytes;
   return cudaLaunchKernelEx(&cfg, cache_chunk_kernel<D, CAP, ONE>, p);
+}
+
+template <int D, bool ONE>
+cudaError_t launch_units(const ChunkParams& p, int cap, const cudaLaunchConfig_t& cfg) {
+  return cap == kCapAny     ? launch_units<D, kCapAny, ONE>(p, cfg)
+         : cap == kCapUsual ? launch_units<D, kCapUsual, ONE>(p, cfg)
+                            : launch_units<D, kCapNone, ONE>(p, cfg);
 }
 
 template <int D>
@@ -917,7 +918,7 @@ cudaError_t launch_chunk(const ChunkParams& p, const ChunkSplit& t, cudaStream_t
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const bool cap = p.a.softcap > 0.f;
+  const int cap = cap_kind(p.a.softcap);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -926,8 +927,7 @@ cudaError_t launch_chunk(const ChunkParams& p, const ChunkSplit& t, cudaStream_t
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = p.direct ? 0 : 1;
-  e = t.one ? (cap ? launch_units<D, true, true>(p, cfg) : launch_units<D, false, true>(p, cfg))
-            : (cap ? launch_units<D, true, false>(p, cfg) : launch_units<D, false, false>(p, cfg));
+  e = t.one ? launch_units<D, true>(p, cap, cfg) : launch_units<D, false>(p, cap, cfg);
   if (e != cudaSuccess || !t.split || p.num_runs < 2) return e;
   cfg.gridDim = dim3(p.num_runs - 1, kUnitRows / 8);
   cfg.blockDim = dim3(256);

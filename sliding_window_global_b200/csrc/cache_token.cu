@@ -257,7 +257,7 @@ __device__ __forceinline__ void join_unit(const CacheAttendParams& p, const Cach
   cluster_sync();                                      // nobody leaves while its memory is read
 }
 
-template <int D, int MT, bool CAP, bool UNIT>
+template <int D, int MT, int CAP, bool UNIT>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __grid_constant__ CacheAttendParams p,
                                                                          int cluster) {
   using S = Step<D>;
@@ -369,8 +369,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
 
   // ---- computing side
   const float sl2 = p.scale * kLog2e;
-  const float cap_l2 = p.softcap * kLog2e;             // CAP: cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
-  const float cap_in = CAP ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
+  const ScoreCap<CAP> score_cap(sl2, p.softcap);
   int done = 0;
   while (UNIT || done < total) {
     const TokenUnit u = UNIT ? unit : token_unit<D>(p, b);
@@ -448,11 +447,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_token_kernel(const __
         float mx[2] = {m[mt][0], m[mt][1]};
 #pragma unroll
         for (int t = 0; t < 2 * NG; ++t) {
+          if (CAP) {
+            score_cap.pair(s[mt][t][0], s[mt][t][1]);
+            score_cap.pair(s[mt][t][2], s[mt][t][3]);
+          }
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float x = s[mt][t][c];
-            if (CAP) x = cap_l2 - 2.f * cap_l2 * rcp_approx(1.f + ex2_approx(x * cap_in));
-            else x *= sl2;
+            float x = CAP ? s[mt][t][c] : s[mt][t][c] * sl2;
             if (masked) {
               const int key = key0 + 8 * t + 2 * (lane & 3) + (c & 1);
               const bool see = key >= klo[mt][c >> 1] && key < khi[mt][c >> 1] && (pages >> (NG - 1 - t / 2) & 1);
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_token_merge_kernel(const 
   if (p.lse && c == 0) p.lse[row] = has ? top + log2f(sum) * kLn2 : -INFINITY;
 }
 
-template <int D, int MT, bool CAP>
+template <int D, int MT, int CAP>
 cudaError_t launch_token(const CacheAttendParams& p, const TokenSplit& t, cudaStream_t s) {
   const int smem = t.warps * kStages * Step<D>::kBytes;
   cudaLaunchConfig_t cfg = {};
@@ -670,6 +671,14 @@ cudaError_t launch_token(const CacheAttendParams& p, const TokenSplit& t, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, many ? cache_token_merge_kernel<D, 128> : cache_token_merge_kernel<D, 512>, p,
                             t.blocks * t.warps, 16 * MT);
+}
+
+template <int D, int MT>
+cudaError_t launch_token(const CacheAttendParams& p, const TokenSplit& t, cudaStream_t s) {
+  const int cap = cap_kind(p.softcap);
+  return cap == kCapAny     ? launch_token<D, MT, kCapAny>(p, t, s)
+         : cap == kCapUsual ? launch_token<D, MT, kCapUsual>(p, t, s)
+                            : launch_token<D, MT, kCapNone>(p, t, s);
 }
 
 // Shared memory of the joined parts fits into the rings they replace.
@@ -734,13 +743,8 @@ cudaError_t launch_cache_token(CacheAttendParams p, const TokenSplit& t, void* w
   p.prefix = static_cast<int*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + (((size_t)p.B + 1) * 4 + 15) / 16 * 16);
   p.part_lse = p.part_o + (size_t)2 * t.blocks * t.warps * t.row_pad * p.D;
-  const bool cap = p.softcap > 0.f;
-  if (p.D == 64) {
-    if (t.row_pad == 16) return cap ? launch_token<64, 1, true>(p, t, s) : launch_token<64, 1, false>(p, t, s);
-    return cap ? launch_token<64, 2, true>(p, t, s) : launch_token<64, 2, false>(p, t, s);
-  }
-  if (t.row_pad == 16) return cap ? launch_token<128, 1, true>(p, t, s) : launch_token<128, 1, false>(p, t, s);
-  return cap ? launch_token<128, 2, true>(p, t, s) : launch_token<128, 2, false>(p, t, s);
+  if (p.D == 64) return t.row_pad == 16 ? launch_token<64, 1>(p, t, s) : launch_token<64, 2>(p, t, s);
+  return t.row_pad == 16 ? launch_token<128, 1>(p, t, s) : launch_token<128, 2>(p, t, s);
 }
 
 }  // namespace swa
