@@ -504,7 +504,8 @@ typedef struct {
   const void* q;               /* device [T, Hq, D], strides (token, head), positive */
   int64_t q_stride[2];
   int max_tokens;              /* no sequence has more new tokens (ignored without cu_tokens) */
-  int max_len;                 /* no seq_lens[b] is larger; 0: max_pages * page_size */
+  int max_len;                 /* no seq_lens[b] is larger; 0: max_pages * page_size.  Never
+                                  above 2^31 - 256, where the attention's positions end */
   int window;                  /* one-sided radius >= 0, or -1: no window */
   float softcap;               /* 0: none */
   float scale;                 /* 0 selects 1/sqrt(head_dim) */

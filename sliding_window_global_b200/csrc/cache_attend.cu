@@ -645,6 +645,10 @@ AttendSplit attend_split(const swa_cache& c, const swa_cache_batch& b, const swa
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// The longest sequence: the kernels' key numbers run past a sequence's end by less than
+// 256 (a tile, or the steps fetched ahead) and have to stay in an int.
+constexpr long long kLongest = 0x7fffffffLL - 255;
+
 // Sizes of an attend call, checked: the status, and the bounds the kernels use.
 swa_status attend_bounds(const swa_cache& c, const swa_cache_batch& b, const swa_cache_attend_args& a, int* max_tokens,
                          int* max_len) {
@@ -658,7 +662,7 @@ swa_status attend_bounds(const swa_cache& c, const swa_cache_batch& b, const swa
   if (a.num_q_heads > kMaxHeads) return SWA_ERR_UNSUPPORTED;
   const long long capacity = (long long)b.max_pages * c.page_size;
   *max_tokens = b.cu_tokens ? std::min(a.max_tokens, b.num_tokens) : (b.batch ? b.num_tokens / b.batch : 0);
-  *max_len = (int)std::min<long long>(a.max_len ? a.max_len : capacity, capacity);
+  *max_len = (int)std::min<long long>({a.max_len ? a.max_len : capacity, capacity, kLongest});
   if ((long long)b.batch * *max_tokens * a.num_q_heads > 0x7fffffffLL ||
       (long long)b.num_tokens * a.num_q_heads > 0x7fffffffLL)
     return SWA_ERR_UNSUPPORTED;

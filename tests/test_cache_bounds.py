@@ -6,7 +6,7 @@ import random
 import pytest
 import torch
 
-from sliding_window_global_b200 import load_library
+from sliding_window_global_b200 import PagedCache, load_library
 from sliding_window_global_b200.cache import Cache, CacheAttendArgs, CacheBatch
 from tests.test_cache import _problem, check_attention, reference
 
@@ -66,6 +66,25 @@ def test_only_pages_in_reach_are_looked_up(D):
         assert looked_up(D, page, 2000 // page + 1, [length], [c], window, 0, c) == [(keys[0] // page, keys[-1] // page)]
 
 
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("page,columns", [(16, 2 ** 27), (65536, 2 ** 15), (65536, 2 ** 15 + 1), (65536, 2 ** 20)])
+def test_capacities_beyond_int32_bound_nothing(dtype, page, columns):
+    """A table of 2^31 positions or more: split as for the longest length that an int32 holds."""
+    lib = load_library()
+
+    def workspace(columns, max_len=0):
+        c = Cache(_PTR, _PTR, 8, 1, page, 64, dtype, _PTR)
+        b = CacheBatch(1, 1, _PTR, columns, _PTR, None)
+        a = CacheAttendArgs(num_q_heads=4, q=_PTR, q_stride0=256, q_stride1=64, max_len=max_len, window=-1, out=_PTR)
+        return lib.swa_cache_attend_workspace_bytes(ctypes.byref(c), ctypes.byref(b), ctypes.byref(a))
+
+    assert workspace(columns) == workspace(columns, 2 ** 31 - 1) == workspace(columns, 2 ** 31 - 256) > 0
+    if dtype == 0:
+        assert looked_up(64, page, columns, [2000], [1], 100, 0, 1) == [(1899 // page, 1999 // page)]
+        top = 2 ** 31 - 256
+        assert looked_up(64, page, columns, [top], [1], 100, 0, 1) == [((top - 101) // page, (top - 1) // page)]
+
+
 # kernels: few tokens (clusters, runs), many tokens (with a list of units, without), fp32 few and many
 KERNELS = [
     ("cluster", BF16, 4, 1, 64, 16, 100, [1, 2, 1], [300, 200, 77]),
@@ -121,3 +140,30 @@ def test_entries_before_the_windows_may_hold_anything(D, dtype, G, new, page):
                                      **bounds)
         assert s["cache"].check() == 0
         check_attention(out, lse, ref, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,new,G", [(BF16, 1, 4), (BF16, 200, 2), (BF16, 20, 8), (FP32, 1, 4), (FP32, 90, 2)])
+def test_a_table_of_two_billion_positions(dtype, new, G):
+    """Two pages of 65536 positions, named in turn by a table that passes 2^31: short lengths
+    without a bound on them, and the longest ones, behind a window."""
+    page, D = 65536, 64
+    g = torch.Generator().manual_seed(61)
+    k, v = (torch.randn((2, 1, page, D), generator=g).to(dtype).cuda() for _ in range(2))
+    table = (torch.arange(2 ** 15 + 1, dtype=torch.int32) % 2)[None]
+    cache = PagedCache(k, v)
+    q = torch.randn((new, G, D), generator=g).to(dtype).cuda()
+    s = dict(k=k, v=v, table=table, page=page, new=[new], cu=torch.tensor([0, new]), total=new)
+    for length, window in ((1000, None), (1000, 70), (2 ** 31 - 256, 70), (2 ** 31 - 65536 + 30, 70)):
+        s["lens"] = torch.tensor([length], dtype=torch.int32)
+        out, lse = cache.attend(q, s["lens"].cuda(), table.cuda(), window=window)
+        assert cache.check() == 0
+        check_attention(out, lse, reference(s, q, window, 0.0, 0.0, G), dtype)
+    # positions from 2^31 - 256 on are beyond every bound of the attention
+    cache.attend(q, torch.tensor([2 ** 31 - 255], dtype=torch.int32, device="cuda"), table.cuda(), window=70)
+    assert cache.check() == DEVICE_CHECK
+    at = 2 ** 31 - 256 - new
+    rows = torch.randn((new, 1, D), generator=g).to(dtype).cuda()
+    cache.append(rows, rows, torch.tensor([at + new], dtype=torch.int32, device="cuda"), table.cuda())
+    assert cache.check() == 0
+    assert torch.equal(v[int(table[0, at // page]), 0, at % page:at % page + new], rows[:, 0])
