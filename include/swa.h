@@ -380,7 +380,8 @@ typedef struct {
   const void* q;
   const void* k;
   int64_t q_stride[3], k_stride[3];
-  const int32_t* positions;   /* device [B, n], or NULL: start, start + 1, ... in every batch */
+  const int32_t* positions;   /* device [B, n], or NULL: start, start + 1, ..., start + n - 1 in every
+                                 batch, the last one still an int32 (else SWA_ERR_INVALID_ARG) */
   int start;
   void* q_out;
   void* k_out;

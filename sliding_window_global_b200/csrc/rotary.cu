@@ -454,6 +454,11 @@ bool no_overlap(const int64_t* st, const long long* size, int dims, int D) {
   return true;
 }
 
+// Positions counted from `start` have to stay in an int32.
+bool positions_ok(const int32_t* positions, int start, int n) {
+  return positions || (long long)start + n - 1 <= 0x7fffffffLL;
+}
+
 swa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA; }
 
 }  // namespace
@@ -519,6 +524,7 @@ swa_status swa_rotary_forward(const swa_rotary_args* a, void* stream) {
   const long long tokens = (long long)a->batch * a->seq_len;
   if (tokens > 0x7fffffffLL - 64) return SWA_ERR_UNSUPPORTED;
   if (tokens == 0) return SWA_OK;
+  if (!swa::positions_ok(a->positions, a->start, a->seq_len)) return SWA_ERR_INVALID_ARG;
   const long long qs[3] = {a->batch, a->num_q_heads, a->seq_len}, ks[3] = {a->batch, Hk, a->seq_len};
   if (!a->q || !a->q_out || !swa::aligned16(a->q) || !swa::aligned16(a->q_out) || !swa::aligned4(a->positions) ||
       !swa::strides_ok(a->q_stride, qs, 3, a->dtype) || !swa::strides_ok(a->q_out_stride, qs, 3, a->dtype) ||
@@ -609,6 +615,7 @@ swa_status swa_rotary_backward(const swa_rotary_backward_args* a, void* stream) 
     if (dweight[0] || dweight[1]) swa::zero_weight_kernel<<<1, 128, 0, s>>>(dweight[0], dweight[1], D);
     return swa::cuda_status(cudaGetLastError());
   }
+  if (!swa::positions_ok(a->positions, a->start, a->seq_len)) return SWA_ERR_INVALID_ARG;
   const long long qs[3] = {a->batch, a->num_q_heads, a->seq_len}, ks[3] = {a->batch, Hk, a->seq_len};
   if (!a->dq_out || !a->dq || !swa::aligned16(a->dq_out) || !swa::aligned16(a->dq) || !swa::aligned4(a->positions) ||
       !swa::strides_ok(a->dq_out_stride, qs, 3, a->grad_dtype) || !swa::strides_ok(a->dq_stride, qs, 3, a->out_dtype) ||

@@ -1,0 +1,36 @@
+"""The rotation's arguments at the edge of what the library's types hold."""
+import ctypes
+
+import pytest
+import torch
+
+from sliding_window_global_b200 import Rotary, SwaError, load_library
+from sliding_window_global_b200.rotary import RotaryArgs, RotaryBackwardArgs
+from tests.test_rotary import _args
+
+INVALID = 1
+
+
+@pytest.mark.parametrize("cls,entry", [(RotaryArgs, "swa_rotary_forward"), (RotaryBackwardArgs, "swa_rotary_backward")])
+def test_positions_that_pass_int32_are_refused(cls, entry):
+    """start, start + 1, ... must not wrap to negative positions."""
+    call = getattr(load_library(), entry)
+    for start, n in ((2 ** 31 - 1, 2), (2 ** 31 - 5, 6), (1, 2 ** 31 - 65)):
+        assert call(ctypes.byref(_args(cls, start=start, seq_len=n)), None) == INVALID
+
+
+@pytest.mark.gpu
+def test_the_last_positions():
+    """start up to the last int32, and a start that is not used beside positions."""
+    g = torch.Generator().manual_seed(67)
+    r = Rotary(64)
+    x = torch.randn((1, 2, 9, 64), generator=g).cuda()
+    pos = (2 ** 31 - 9 + torch.arange(9)).to(torch.int32)[None].cuda()
+    want, _ = r.forward(x, positions=pos)
+    assert torch.equal(r.forward(x, start=2 ** 31 - 9)[0], want)
+    assert torch.equal(r.forward(x, positions=pos, start=2 ** 31 - 1)[0], want)
+    assert torch.equal(r.backward(x, start=2 ** 31 - 9)[0], r.backward(x, positions=pos, start=2 ** 31 - 1)[0])
+    for call in (r.forward, r.backward):
+        with pytest.raises(SwaError) as e:
+            call(x, start=2 ** 31 - 8)
+        assert e.value.status == INVALID
