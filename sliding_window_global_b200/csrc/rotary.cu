@@ -612,7 +612,8 @@ swa_status swa_rotary_backward(const swa_rotary_backward_args* a, void* stream) 
   const long long tokens = (long long)a->batch * a->seq_len;
   float* dweight[2] = {norm ? a->dq_weight : nullptr, norm ? a->dk_weight : nullptr};
   if (tokens == 0) {
-    if (dweight[0] || dweight[1]) swa::zero_weight_kernel<<<1, 128, 0, s>>>(dweight[0], dweight[1], D);
+    if (!dweight[0] && !dweight[1]) return SWA_OK;
+    swa::zero_weight_kernel<<<1, 128, 0, s>>>(dweight[0], dweight[1], D);
     return swa::cuda_status(cudaGetLastError());
   }
   if (!swa::positions_ok(a->positions, a->start, a->seq_len)) return SWA_ERR_INVALID_ARG;

@@ -34,3 +34,11 @@ def test_the_last_positions():
         with pytest.raises(SwaError) as e:
             call(x, start=2 ** 31 - 8)
         assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("cls,entry", [(RotaryArgs, "swa_rotary_forward"), (RotaryBackwardArgs, "swa_rotary_backward")])
+@pytest.mark.parametrize("empty", [dict(batch=0), dict(seq_len=0)])
+def test_a_call_without_rows_has_no_status_of_others(cls, entry, empty):
+    """Nothing is launched, so nothing that the CUDA runtime remembers is reported (here: that
+    there is no device)."""
+    assert getattr(load_library(), entry)(ctypes.byref(_args(cls, start=2 ** 31 - 1, **empty)), None) == 0
