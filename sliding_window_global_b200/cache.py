@@ -10,8 +10,8 @@ from typing import Optional
 
 import torch
 
-from .rotary import (F, I, I64, NO_ROTATION, P, HeadNorm, Rotary, Rotation, check_index, check_rows, current_stream,
-                     elsewhere, head_norm, packer)
+from .rotary import (F, I, I64, NO_ROTATION, P, HeadNorm, Rotary, Rotation, check_fp32, check_index, check_rows,
+                     current_stream, elsewhere, head_norm, packer)
 from .swa import SwaError, _dtype_code, load_library
 
 
@@ -170,6 +170,8 @@ class PagedCache:
             window = -1
         elif window < 0:
             raise ValueError("window must be None or at least 0")
+        check_fp32(softcap, "softcap")
+        check_fp32(scale, "scale")
         # bounds beyond what an int32 length can reach bound nothing
         window = min(window, _INT_MAX)
         max_len = min(max_len, _INT_MAX)

@@ -160,6 +160,13 @@ def head_norm(norm_eps, q_weight, k_weight, head_dim: int, device):
     return 1, norm_eps, ptrs[0], ptrs[1], code
 
 
+def check_fp32(x: float, name: str):
+    """A number the library takes as fp32 and for which 0 means something of its own: refused
+    where fp32 would round it to 0 or to infinity."""
+    if x and math.isfinite(x) and ctypes.c_float(x).value in (0.0, math.inf, -math.inf):
+        raise ValueError(f"{name} is outside the range of fp32: {x}")
+
+
 def check_start(start: int):
     if not -2 ** 31 <= start < 2 ** 31:
         raise ValueError(f"start must be an int32, got {start}")
@@ -219,6 +226,7 @@ class Rotary:
                              f"got {head_dim} and {self.rotary_dim}")
         if not math.isfinite(self.amplitude) or self.amplitude == 0.0:
             raise ValueError("amplitude must be finite and not zero")
+        check_fp32(self.amplitude, "amplitude")
         if frequencies is None:
             frequencies = rotary_frequencies(self.rotary_dim)[0] if self.rotary_dim else torch.empty(0)
         freq = frequencies.detach().to("cpu", torch.float64).reshape(-1).tolist()

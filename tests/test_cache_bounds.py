@@ -167,3 +167,19 @@ def test_a_table_of_two_billion_positions(dtype, new, G):
     cache.append(rows, rows, torch.tensor([at + new], dtype=torch.int32, device="cuda"), table.cuda())
     assert cache.check() == 0
     assert torch.equal(v[int(table[0, at // page]), 0, at % page:at % page + new], rows[:, 0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["scale", "softcap"])
+def test_numbers_that_fp32_does_not_hold_are_refused(name):
+    """Rounded to 0 a scale would stand for the default, a cap for none."""
+    p = torch.randn((2, 1, 16, 64), device="cuda")
+    cache = PagedCache(p, p.clone())
+    lens, table = torch.full((1,), 20, dtype=torch.int32, device="cuda"), torch.tensor([[0, 1]], dtype=torch.int32).cuda()
+    q = torch.randn((1, 2, 64), device="cuda")
+    for value in (1e-50, 1e-46, 1e39):
+        with pytest.raises(ValueError):
+            cache.attend(q, lens, table, **{name: value})
+    out, _ = cache.attend(q, lens, table, **{name: 1e-40})           # every score alike
+    assert float((out - out[:, :1]).abs().max()) <= 2.0 ** -20 * float(p.abs().max())
+    assert cache.check() == 0

@@ -42,3 +42,11 @@ def test_a_call_without_rows_has_no_status_of_others(cls, entry, empty):
     """Nothing is launched, so nothing that the CUDA runtime remembers is reported (here: that
     there is no device)."""
     assert getattr(load_library(), entry)(ctypes.byref(_args(cls, start=2 ** 31 - 1, **empty)), None) == 0
+
+
+@pytest.mark.parametrize("amplitude", [1e-50, -1e-46, 1e39, -1e300])
+def test_amplitudes_that_fp32_does_not_hold_are_refused(amplitude):
+    """Rounded to 0 an amplitude would stand for the default, 1."""
+    with pytest.raises(ValueError):
+        Rotary(64, amplitude=amplitude)
+    assert Rotary(64, amplitude=1e-40).amplitude == 1e-40
