@@ -583,6 +583,17 @@ cudaError_t launch_merge(const CacheAttendParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, p.D == 64 ? cache_merge_kernel<64> : cache_merge_kernel<128>, p);
 }
 
+// A call that allows no sequence a token computes nothing: its bounds are checked all the same.
+__global__ void cache_bounds_kernel(const __grid_constant__ CacheAttendParams p) {
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x)
+    if (cache_seq(p, b).bad) atomicOr(p.err, kDevErrCheck);
+}
+
+cudaError_t launch_bounds(const CacheAttendParams& p, cudaStream_t s) {
+  cache_bounds_kernel<<<1, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
 // How a call is cut up, from sizes only: which kernel, and its parts.
 struct AttendSplit {
   enum { kToken, kChunk, kCore } kernel;
@@ -736,7 +747,12 @@ swa_status swa_cache_attend(const swa_cache* c, const swa_cache_batch* b, const 
   swa::CacheAttendParams p = {};
   const swa_status st = swa::attend_bounds(*c, *b, *a, &p.max_tokens, &p.max_len);
   if (st != SWA_OK) return st;
-  if (b->batch == 0 || b->num_tokens == 0 || p.max_tokens == 0) return SWA_OK;
+  if (b->batch == 0 || b->num_tokens == 0) return SWA_OK;
+  if (p.max_tokens == 0) {
+    swa::fill_params(*c, *b, *a, &p);
+    const cudaError_t e = swa::launch_bounds(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+  }
   const int64_t unit = c->dtype == SWA_FP32 ? 4 : 8;
   if (!a->q || !a->out || !swa::aligned16(a->q) || !swa::aligned16(a->out) || !swa::aligned4(a->lse) ||
       (b->num_tokens > 1 && (a->q_stride[0] <= 0 || a->q_stride[0] % unit)) ||

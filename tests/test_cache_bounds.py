@@ -183,3 +183,17 @@ def test_numbers_that_fp32_does_not_hold_are_refused(name):
     out, _ = cache.attend(q, lens, table, **{name: 1e-40})           # every score alike
     assert float((out - out[:, :1]).abs().max()) <= 2.0 ** -20 * float(p.abs().max())
     assert cache.check() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_a_bound_of_no_tokens_is_reported_where_it_does_not_hold(dtype):
+    s = _problem(dtype, 2, 64, 16, [0, 3, 0], [0, 30, 40], 71)
+    q = torch.randn((3, 4, 64), generator=s["g"]).to(dtype).cuda()
+    out, lse = torch.full_like(q, 7.0), torch.full((3, 4), 7.0, device="cuda")
+    args = (q, s["lens"].cuda(), s["table"].cuda())
+    s["cache"].attend(*args, cu_tokens=s["cu"].cuda(), max_tokens=0, out=out, lse=lse)
+    assert s["cache"].check() == DEVICE_CHECK
+    s["cache"].attend(*args, cu_tokens=torch.zeros(4, dtype=torch.int32, device="cuda"), max_tokens=0, out=out, lse=lse)
+    assert s["cache"].check() == 0                         # rows of no sequence only
+    assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
