@@ -58,7 +58,9 @@ class PagedCache:
     ``cu_tokens`` int32 [B + 1] gives each sequence's rows (None: T / B rows each), and
     ``seq_lens`` int32 [B] the sequences' lengths with the new tokens.  ``block_table`` is
     int32 [B, max_pages].  These stay on the device and are not read by the host: a page or
-    position that does not exist is left out, and ``check()`` reports it."""
+    position that does not exist is left out, and ``check()`` reports it.
+
+    ``k_pages`` and ``v_pages`` stay the tensors that the cache was made of."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor):
         self._lib = load_library()
@@ -74,12 +76,27 @@ class PagedCache:
         if self.head_dim not in (64, 128) or self.page_size % 16 or min(pages, self.num_kv_heads, self.page_size) < 1:
             raise ValueError("a cache needs pages and heads, a head_dim of 64 or 128 and a page_size that is a "
                              f"multiple of 16, got {tuple(k_pages.shape)}")
-        self.k_pages, self.v_pages, self.dtype = k_pages, v_pages, k_pages.dtype
+        self._k_pages, self._v_pages, self.dtype = k_pages, v_pages, k_pages.dtype
         self._error = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
-        self._cache = Cache(k_pages.data_ptr(), v_pages.data_ptr(), pages, self.num_kv_heads, self.page_size,
-                            self.head_dim, _dtype_code(self.dtype), self._error.data_ptr())
+        self._at = k_pages.data_ptr(), v_pages.data_ptr()
+        self._cache = Cache(*self._at, pages, self.num_kv_heads, self.page_size, self.head_dim,
+                            _dtype_code(self.dtype), self._error.data_ptr())
         self._ref = bytes(self._cache)
         self._device = k_pages.device
+
+    @property
+    def k_pages(self) -> torch.Tensor:
+        return self._k_pages
+
+    @property
+    def v_pages(self) -> torch.Tensor:
+        return self._v_pages
+
+    def _enter(self, stream):
+        # the library holds the pages' addresses
+        if (self._k_pages.data_ptr(), self._v_pages.data_ptr()) != self._at:
+            raise ValueError("the pages have moved in memory; make a new PagedCache of them")
+        return elsewhere(self._k_pages, "k_pages", stream)
 
     def _rows(self, t, name, T=None, heads=None):
         strides = check_rows(t, name, self._device, 3, self.dtype)
@@ -109,7 +126,7 @@ class PagedCache:
         the pages, k normed (``norm_eps``, as in ``Rotary.forward``) and rotated at its
         position; q [T, Hq, D] is normed and rotated alike into ``q_out``, which is returned
         (it may be q; rows of no sequence are not written)."""
-        ctx = elsewhere(self.k_pages, "k_pages", stream)
+        ctx = self._enter(stream)
         if ctx is None:
             return self._append(k, v, seq_lens, block_table, q, cu_tokens, rotary, norm_eps, q_weight, k_weight, q_out)
         with ctx:
@@ -138,7 +155,7 @@ class PagedCache:
             Hq, q_ptr, k.data_ptr(), v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qo_ptr, os[0], os[1],
             *(NO_ROTATION if rotary is None else rotary.fields),
             *head_norm(norm_eps, q_weight, k_weight, self.head_dim, self._device))
-        st = self._lib.swa_cache_append(self._ref, batch, a, current_stream(self.k_pages))
+        st = self._lib.swa_cache_append(self._ref, batch, a, current_stream(self._k_pages))
         if st != 0:
             raise SwaError(st, "swa_cache_append")
         return q_out
@@ -155,7 +172,7 @@ class PagedCache:
         capacity).  ``softcap`` c > 0 turns a score s into ``c tanh(s / c)``; scale 0 is
         1/sqrt(D).  Returns ``(out, lse)``: [T, Hq, D] and fp32 [T, Hq] (natural log); rows of
         no sequence are not written."""
-        ctx = elsewhere(self.k_pages, "k_pages", stream)
+        ctx = self._enter(stream)
         args = (q, seq_lens, block_table, cu_tokens, max_tokens, max_len, window, softcap, scale, out, lse, return_lse)
         if ctx is None:
             return self._attend(*args)
@@ -196,15 +213,15 @@ class PagedCache:
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=self._device)
             a = _pack_attend(*fields, ws.data_ptr(), need)
-        st = self._lib.swa_cache_attend(self._ref, batch, a, current_stream(self.k_pages))
+        st = self._lib.swa_cache_attend(self._ref, batch, a, current_stream(self._k_pages))
         if st != 0:
             raise SwaError(st, "swa_cache_attend")
         return out, lse
 
     def check(self, stream=None) -> int:
         """Synchronise, read and clear the cache's error word (0 = OK)."""
-        ctx = elsewhere(self.k_pages, "k_pages", stream)
+        ctx = elsewhere(self._k_pages, "k_pages", stream)
         if ctx is None:
-            return int(self._lib.swa_cache_check(self._ref, current_stream(self.k_pages)))
+            return int(self._lib.swa_cache_check(self._ref, current_stream(self._k_pages)))
         with ctx:
-            return int(self._lib.swa_cache_check(self._ref, current_stream(self.k_pages)))
+            return int(self._lib.swa_cache_check(self._ref, current_stream(self._k_pages)))

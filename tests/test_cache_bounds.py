@@ -197,3 +197,28 @@ def test_a_bound_of_no_tokens_is_reported_where_it_does_not_hold(dtype):
     s["cache"].attend(*args, cu_tokens=torch.zeros(4, dtype=torch.int32, device="cuda"), max_tokens=0, out=out, lse=lse)
     assert s["cache"].check() == 0                         # rows of no sequence only
     assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+
+
+def test_a_cache_keeps_its_pages():
+    """The kernels use the addresses of the pages that the cache was made of."""
+    cache = object.__new__(PagedCache)
+    for name in ("k_pages", "v_pages"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, torch.zeros(1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["k_pages", "v_pages"])
+def test_pages_that_moved_are_refused(name):
+    p = torch.zeros((2, 1, 16, 64), device="cuda")
+    cache = PagedCache(p, p.clone())
+    lens, table = torch.ones(1, dtype=torch.int32, device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    k = torch.ones((1, 1, 64), device="cuda")
+    cache.append(k, k, lens, table)
+    old = getattr(cache, name).clone()
+    assert float(old.sum()) == 64
+    getattr(cache, name).data = old                        # the same tensor in other memory
+    for call in (lambda: cache.append(k, k, lens, table), lambda: cache.attend(k, lens, table)):
+        with pytest.raises(ValueError):
+            call()
+    assert cache.check() == 0
