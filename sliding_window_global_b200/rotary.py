@@ -205,6 +205,10 @@ def rotary_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str =
     raise ValueError(f"unknown scaling {scaling!r}; use none, linear, ntk or yarn")
 
 
+def _make(head_dim, options):
+    return Rotary(head_dim, **options)
+
+
 class Rotary:
     """Rotation of query and key heads by their positions, with an optional RMS norm of
     every head before it, and its gradients.
@@ -234,6 +238,12 @@ class Rotary:
             raise ValueError(f"frequencies needs {self.rotary_dim // 2} finite values")
         self._freq = (ctypes.c_double * max(1, len(freq)))(*freq)
         self.fields = (self.rotary_dim, int(self.interleaved), ctypes.addressof(self._freq), self.amplitude)
+
+    def __reduce__(self):
+        # a copy has its own frequencies, and the library belongs to the process
+        freq = torch.tensor(self._freq[:self.rotary_dim // 2], dtype=torch.float64)
+        return _make, (self.head_dim, dict(rotary_dim=self.rotary_dim, interleaved=self.interleaved, frequencies=freq,
+                                           amplitude=self.amplitude))
 
     def forward(self, q: torch.Tensor, k: Optional[torch.Tensor] = None, *, positions: Optional[torch.Tensor] = None,
                 start: int = 0, norm_eps: Optional[float] = None, q_weight: Optional[torch.Tensor] = None,

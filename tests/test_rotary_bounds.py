@@ -1,10 +1,12 @@
 """The rotation's arguments at the edge of what the library's types hold."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
 
-from sliding_window_global_b200 import Rotary, SwaError, load_library
+from sliding_window_global_b200 import Rotary, SwaError, load_library, rotary_frequencies
 from sliding_window_global_b200.rotary import RotaryArgs, RotaryBackwardArgs
 from tests.test_rotary import _args
 
@@ -50,3 +52,15 @@ def test_amplitudes_that_fp32_does_not_hold_are_refused(amplitude):
     with pytest.raises(ValueError):
         Rotary(64, amplitude=amplitude)
     assert Rotary(64, amplitude=1e-40).amplitude == 1e-40
+
+
+def test_a_rotation_can_be_copied_and_pickled():
+    """As a module that holds one is."""
+    freq, amp = rotary_frequencies(48, scaling="yarn", factor=8.0)
+    r = Rotary(64, rotary_dim=48, interleaved=False, frequencies=freq, amplitude=amp)
+    for other in (copy.copy(r), copy.deepcopy(r), pickle.loads(pickle.dumps(r))):
+        assert isinstance(other, Rotary) and other is not r
+        assert (other.head_dim, other.rotary_dim, other.interleaved, other.amplitude) == (64, 48, False, amp)
+        at, size = other.fields[2], 24
+        assert list((ctypes.c_double * size).from_address(at)) == freq.tolist()
+    assert copy.deepcopy(Rotary(128, rotary_dim=0)).rotary_dim == 0
