@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import hashlib
 import os
 import subprocess
 import sys
@@ -43,8 +44,10 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not needs_build():
         return LIB
     # one nvcc per source, side by side; objects newer than their source and every
-    # header are kept
+    # header are kept, those of a build with extra flags in a folder of their own
     objdir = os.path.join(HERE, "_build")
+    if extra:
+        objdir = os.path.join(objdir, hashlib.sha256("\0".join(extra).encode()).hexdigest()[:16])
     os.makedirs(objdir, exist_ok=True)
     hdr = max(os.path.getmtime(f) for f in headers() + [os.path.abspath(__file__)])
     flags = [f for f in FLAGS if f not in LINK_FLAGS]
