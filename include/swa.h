@@ -348,7 +348,8 @@ swa_status swa_forward_noalloc(const swa_plan_desc* desc, const void* q, const v
  *   y[a] = A (u[a] cos - u[b] sin),  y[b] = A (u[a] sin + u[b] cos),  angle = t * freq[j]
  * for every pair j < rotary_dim / 2: (a, b) = (2j, 2j + 1) in the interleaved
  * layout, (j, j + rotary_dim / 2) in the half layout; elements from rotary_dim on
- * keep u.  Angles are formed in 64 bits, sums in 32, and y is rounded once.
+ * keep u.  Angles are formed modulo one turn in 64-bit fixed point and used to 2^-32 turns,
+ * sums are in 32 bits, and y is rounded once.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int rotary_dim;          /* leading elements of the head that rotate: a multiple of 16,
@@ -491,10 +492,12 @@ swa_status swa_cache_append(const swa_cache* cache, const swa_cache_batch* batch
                             const swa_cache_append_args* args, void* stream);
 
 /* Attention of the new tokens' queries over the cache (which holds their own keys
- * already): query head h of a token at position t attends, with KV head
+ * already), with one window for all heads and without dilation: query head h of a token at position t attends, with KV head
  * h / (Hq / Hkv), the positions max(0, t - window) .. t;
  *   s = scale <q, k>, then s = softcap * tanh(s / softcap) when softcap > 0;
  *   out = softmax(s) . V, lse = natural-log logsumexp of s.
+ * Scores, maxima and sums are in 32 bits; with a bf16 cache the exponentials are rounded to
+ * bf16 for their product with V (not in the sum).
  * A token without a key (all its pages bad) gives out = 0 and lse = -inf.  Values at
  * positions that no query of the call's sequence attends never reach a result,
  * whatever they hold (also NaN); a position that some but not all of a sequence's new

@@ -169,9 +169,9 @@ class PagedCache:
         included): each token sees the positions up to its own, the last ``window`` ones
         before it only when that is given.  With ``cu_tokens``, ``max_tokens`` bounds a
         sequence's new tokens (T when None); ``max_len`` bounds ``seq_lens`` (0: the table's
-        capacity).  ``softcap`` c > 0 turns a score s into ``c tanh(s / c)``; scale 0 is
-        1/sqrt(D).  Returns ``(out, lse)``: [T, Hq, D] and fp32 [T, Hq] (natural log); rows of
-        no sequence are not written."""
+        capacity).  One window serves all heads, and there is no dilation.  ``softcap`` c > 0
+        turns a score s into ``c tanh(s / c)``; scale 0 is 1/sqrt(D).  Returns ``(out, lse)``:
+        [T, Hq, D] and fp32 [T, Hq] (natural log); rows of no sequence are not written."""
         ctx = self._enter(stream)
         args = (q, seq_lens, block_table, cu_tokens, max_tokens, max_len, window, softcap, scale, out, lse, return_lse)
         if ctx is None:

@@ -25,12 +25,16 @@ namespace {
 constexpr int kRotaryThreads = 128;
 // Heads of a block at most. Forward, a 2 x 8191-token normed prompt: 57.5 us with 32, 59.7 with
 // 16. Backward, a normed 16384-token prompt: 131 us with 16, whose items the blocks share
-// out evenly, 134 with 8, 143 with 32 (before the products went two an instruction: 56.0 and
+// out evenly, 134 with 8, 143 with 32 (before the products went two an instruction: 56 and
 // 129 us now).
 constexpr int kForwardRun = 32, kBackwardRun = 16;
 // Blocks of an SM that the registers must allow. Forward: four (128 registers; 104.5 us for
 // the plain 32768-token prompt, 106.7 without the bound). Backward: five without a norm; with
-// one the compiler's own choice of 168 registers, since four blocks would spill (131 to 163 us).
+// one the compiler's own choice, since four blocks would spill (131 to 163 us). That is 158 to
+// 168 registers and three blocks an SM for bf16 heads in the interleaved layout, and in the half
+// layout with bf16 upstream gradients; 176 to 186 registers and two blocks in the half layout
+// with fp32 upstream gradients and for fp32 heads. 16384 tokens of 32 + 8 heads, D = 128, bf16
+// heads and fp32 gradients: 129 us interleaved, 164 in the half layout.
 // Append: three, whose look-ups need more registers (normed prompts 45.9 us, 51.6 with four).
 constexpr int kForwardBlocks = 4, kBackwardBlocks = 5, kAppendBlocks = 3;
 

@@ -50,10 +50,11 @@ __device__ __forceinline__ void sincos_quarter(float x, float& s, float& c) {
 }
 
 // cos and sin of t * freq, times amp. The position is a whole number, so the angle in turns
-// can be formed modulo one in fixed point, exactly but for the frequency's own rounding to
-// 2^-65 turns: with t below 2^31 an error below 2^-34 turns. (32-bit floats would leave
-// no digit of it at far positions, and 64-bit ones are slow.) The rest to the nearest
-// quarter turn is cut to 2^-32 turns and rounded to 24 bits, an error below 2^-25.
+// can be formed modulo one in fixed point, exactly but for the frequency, which is cut to
+// 2^-64 turns: with |t| up to 2^31 an error of at most 2^-33 turns. (32-bit floats would leave
+// no digit of it at far positions, and 64-bit ones are slow.) The angle is then cut to 2^-32
+// turns, and its rest to the nearest quarter turn rounded to 24 bits, an error below 2^-25
+// of it.
 __device__ __forceinline__ void rotary_angle(int t, uint64_t turn, float amp, float& c, float& s) {
   const uint32_t at = static_cast<uint32_t>((static_cast<uint64_t>(static_cast<int64_t>(t)) * turn) >> 32);
   const uint32_t k = (at + 0x20000000u) >> 30;             // nearest quarter turn
